@@ -29,7 +29,8 @@ constexpr int kDispatchThreads = 256;  // 8 warps, 8 (token, segment) items per 
 // X_EARLY: load and quantize x before waiting for the preceding kernel
 // (moe_dispatch_after_plan); otherwise x is read after the wait, like every
 // other input (moe_dispatch).
-template <bool X_EARLY>
+// E4M3: codes in 8-bit floating point instead of INT8 (moe_dispatch_f8).
+template <bool X_EARLY, bool E4M3>
 __global__ void __launch_bounds__(kDispatchThreads)
 dispatch_kernel(const uint16_t* __restrict__ x, int T, int H, int k, const int32_t* __restrict__ slot,
                 int8_t* __restrict__ codes, float* __restrict__ scales, int Gs, int32_t* __restrict__ err) {
@@ -56,7 +57,7 @@ dispatch_kernel(const uint16_t* __restrict__ x, int T, int H, int k, const int32
     // before this kernel.
     if (!X_EARLY) grid_dependency_sync();
     const SegLoad ld = load_segment(x, t, H, seg, lane);
-    const SegQuant qz = quantize_segment(ld);
+    const SegQuant qz = quantize_segment<E4M3>(ld);
     MOE_TRACE_MARK(tr_dispatch, 1);
     if (X_EARLY) grid_dependency_sync();
     allow_dependents();
@@ -109,13 +110,14 @@ int trace_symbols_dispatch(void** stamps, void** sms) {
 #endif
 
 cudaError_t launch_dispatch(const uint16_t* x, int T, int H, int k, const int32_t* slot, int8_t* codes,
-                            float* scales, int Gs, int32_t* err, bool x_early, cudaStream_t s, uint64_t* launches) {
+                            float* scales, int Gs, int32_t* err, bool x_early, bool e4m3, cudaStream_t s,
+                            uint64_t* launches) {
     const long long items = (long long)T * ((H + kSegElems - 1) / kSegElems);
     const long long blocks = (items + (kDispatchThreads / 32) - 1) / (kDispatchThreads / 32);
-    cudaError_t e = x_early ? launch_pdl(dispatch_kernel<true>, dim3((unsigned)blocks), dim3(kDispatchThreads), 0, s,
-                                         x, T, H, k, slot, codes, scales, Gs, err)
-                            : launch_pdl(dispatch_kernel<false>, dim3((unsigned)blocks), dim3(kDispatchThreads), 0,
-                                         s, x, T, H, k, slot, codes, scales, Gs, err);
+    const auto kernel = e4m3 ? dispatch_kernel<false, true>
+                             : x_early ? dispatch_kernel<true, false> : dispatch_kernel<false, false>;
+    cudaError_t e = launch_pdl(kernel, dim3((unsigned)blocks), dim3(kDispatchThreads), 0, s, x, T, H, k, slot, codes,
+                               scales, Gs, err);
     if (e == cudaSuccess) *launches += 1;
     return e;
 }

@@ -157,10 +157,17 @@ cudaError_t launch_plan(const float* logits, int T, int E, int P, int k,
                         int32_t* ticket /* zeroed int32, or NULL: always three launches */,
                         cudaStream_t s, uint64_t* launches);
 
-// x_early: read x before waiting for the preceding kernel (see moe_dispatch_after_plan).
+cudaError_t launch_plan_routed(const moe_router& router, const float* bias, const float* logits, int T, int E, int P,
+                               int k, const int32_t* rep_off, const int32_t* rep_ids, int32_t* topk_e, float* gates,
+                               int32_t* phys, int32_t* tile_hist, int32_t* local_rank, int32_t* counts,
+                               int32_t* offsets, int32_t* slot, int32_t* src_token, int32_t* src_k, int32_t* err,
+                               int32_t* ticket, cudaStream_t s, uint64_t* launches);
+
+// x_early: read x before waiting for the preceding kernel (see moe_dispatch_after_plan;
+// INT8 only).  e4m3: E4M3 codes instead of INT8.
 cudaError_t launch_dispatch(const uint16_t* x, int T, int H, int k, const int32_t* slot,
                             int8_t* codes, float* scales, int Gs, int32_t* err, bool x_early,
-                            cudaStream_t s, uint64_t* launches);
+                            bool e4m3, cudaStream_t s, uint64_t* launches);
 
 cudaError_t launch_identity_experts(const int8_t* codes, const float* scales, int rows, int H, int Gs,
                                     uint16_t* ex_out, cudaStream_t s, uint64_t* launches);
@@ -175,5 +182,6 @@ struct moe_pool {
     moe::Geometry geo;
     char* base;                       // device workspace
     int32_t planned_T[moe::kMaxSets]; // T of the last moe_plan per set (-1 = none)
+    bool e4m3[moe::kMaxSets];         // the set's codes were last written by moe_dispatch_f8
     uint64_t launches;
 };

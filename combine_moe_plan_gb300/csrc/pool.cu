@@ -7,6 +7,7 @@
 // workspace, with n_sets copies so consecutive iterations alternate sets.
 // No call allocates; every launch is asynchronous on the caller's stream.
 #include <algorithm>
+#include <cfloat>
 #include <cstdlib>
 #include <cstring>
 #include <vector>
@@ -113,6 +114,52 @@ int check_replica_args(const moe_desc& d, const int32_t* rep_off, const int32_t*
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// A router's fields against the pool's geometry.
+int check_router(const moe_desc& d, const moe_router& r) {
+    if (r.score != MOE_SCORE_SOFTMAX && r.score != MOE_SCORE_SIGMOID) return MOE_ERR_SIZE;
+    if (r.n_group < 1 || r.n_group > 32 || d.E % r.n_group != 0) return MOE_ERR_SIZE;
+    const int size = d.E / r.n_group;
+    if (r.topk_group < 1 || r.topk_group > r.n_group || r.topk_group * size < d.k) return MOE_ERR_SIZE;
+    if (r.group_top < 1 || r.group_top > 2 || r.group_top > size) return MOE_ERR_SIZE;
+    if (!(r.scale > 0.0f) || r.scale > FLT_MAX) return MOE_ERR_SIZE;
+    return MOE_OK;
+}
+
+// moe_plan (router NULL) and moe_plan_routed.
+int plan_call(moe_pool* pool, const moe_router* router, const float* logits, const float* bias, int32_t T,
+              const int32_t* rep_off, const int32_t* rep_ids, int buf, void* stream) {
+    int rc = check_call(pool, T, buf);
+    if (rc != MOE_OK) return rc;
+    const moe_desc& d = pool->geo.d;
+    const SetLayout& L = pool->geo.set[buf];
+    pool->planned_T[buf] = -1;
+    if (T == 0) {  // an empty batch: every expert window is empty
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (cudaMemsetAsync(at<int32_t>(pool, L.counts), 0, (size_t)d.P * sizeof(int32_t), s) != cudaSuccess ||
+            cudaMemsetAsync(at<int32_t>(pool, L.offsets), 0, (size_t)(d.P + 1) * sizeof(int32_t), s) !=
+                cudaSuccess)
+            return MOE_ERR_CUDA;
+        pool->planned_T[buf] = 0;
+        return MOE_OK;
+    }
+    if (logits == nullptr) return MOE_ERR_NULL;
+    if (!aligned16(logits)) return MOE_ERR_ALIGN;
+    if ((rc = check_replica_args(d, rep_off, rep_ids)) != MOE_OK) return rc;
+    const auto launch = [&](auto... a) {
+        return router != nullptr ? launch_plan_routed(*router, bias, a...) : launch_plan(a...);
+    };
+    cudaError_t e = launch(logits, T, d.E, d.P, d.k, rep_off, rep_ids, at<int32_t>(pool, L.topk_e),
+                           at<float>(pool, L.gates), at<int32_t>(pool, L.phys), at<int32_t>(pool, L.tile_hist),
+                           at<int32_t>(pool, L.local_rank), at<int32_t>(pool, L.counts),
+                           at<int32_t>(pool, L.offsets), at<int32_t>(pool, L.slot), at<int32_t>(pool, L.src_token),
+                           at<int32_t>(pool, L.src_k), at<int32_t>(pool, pool->geo.error_word),
+                           at<int32_t>(pool, pool->geo.ticket) + buf, static_cast<cudaStream_t>(stream),
+                           &pool->launches);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    pool->planned_T[buf] = T;
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -210,41 +257,23 @@ MOE_API int moe_replica_check(const int32_t* rep_off, const int32_t* rep_ids, in
 
 MOE_API int moe_plan(moe_pool* pool, const float* logits, int32_t T, const int32_t* rep_off,
                      const int32_t* rep_ids, int buf, void* stream) {
-    int rc = check_call(pool, T, buf);
+    return plan_call(pool, nullptr, logits, nullptr, T, rep_off, rep_ids, buf, stream);
+}
+
+MOE_API int moe_plan_routed(moe_pool* pool, const moe_router* router, const float* logits, const float* bias,
+                            int32_t T, const int32_t* rep_off, const int32_t* rep_ids, int buf, void* stream) {
+    if (pool == nullptr || router == nullptr) return MOE_ERR_NULL;
+    const int rc = check_router(pool->geo.d, *router);
     if (rc != MOE_OK) return rc;
-    const moe_desc& d = pool->geo.d;
-    const SetLayout& L = pool->geo.set[buf];
-    pool->planned_T[buf] = -1;
-    if (T == 0) {  // an empty batch: every expert window is empty
-        cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (cudaMemsetAsync(at<int32_t>(pool, L.counts), 0, (size_t)d.P * sizeof(int32_t), s) != cudaSuccess ||
-            cudaMemsetAsync(at<int32_t>(pool, L.offsets), 0, (size_t)(d.P + 1) * sizeof(int32_t), s) !=
-                cudaSuccess)
-            return MOE_ERR_CUDA;
-        pool->planned_T[buf] = 0;
-        return MOE_OK;
-    }
-    if (logits == nullptr) return MOE_ERR_NULL;
-    if (!aligned16(logits)) return MOE_ERR_ALIGN;
-    if ((rc = check_replica_args(d, rep_off, rep_ids)) != MOE_OK) return rc;
-    cudaError_t e = launch_plan(logits, T, d.E, d.P, d.k, rep_off, rep_ids, at<int32_t>(pool, L.topk_e),
-                                at<float>(pool, L.gates), at<int32_t>(pool, L.phys),
-                                at<int32_t>(pool, L.tile_hist), at<int32_t>(pool, L.local_rank),
-                                at<int32_t>(pool, L.counts), at<int32_t>(pool, L.offsets),
-                                at<int32_t>(pool, L.slot), at<int32_t>(pool, L.src_token),
-                                at<int32_t>(pool, L.src_k), at<int32_t>(pool, pool->geo.error_word),
-                                at<int32_t>(pool, pool->geo.ticket) + buf, static_cast<cudaStream_t>(stream),
-                                &pool->launches);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    pool->planned_T[buf] = T;
-    return MOE_OK;
+    if (bias != nullptr && !aligned16(bias)) return MOE_ERR_ALIGN;
+    return plan_call(pool, router, logits, bias, T, rep_off, rep_ids, buf, stream);
 }
 
 }  // extern "C"
 
 namespace {
 
-int dispatch_call(moe_pool* pool, const uint16_t* x, int32_t T, int buf, bool x_early, void* stream) {
+int dispatch_call(moe_pool* pool, const uint16_t* x, int32_t T, int buf, bool x_early, bool e4m3, void* stream) {
     int rc = check_call(pool, T, buf);
     if (rc != MOE_OK) return rc;
     if (T > 0 && x == nullptr) return MOE_ERR_NULL;
@@ -253,9 +282,10 @@ int dispatch_call(moe_pool* pool, const uint16_t* x, int32_t T, int buf, bool x_
     if (T == 0) return MOE_OK;
     const moe_desc& d = pool->geo.d;
     const SetLayout& L = pool->geo.set[buf];
+    pool->e4m3[buf] = e4m3;
     return cuda_rc(launch_dispatch(x, T, d.H, d.k, at<int32_t>(pool, L.slot), at<int8_t>(pool, L.codes),
                                    at<float>(pool, L.scales), pool->geo.Gs,
-                                   at<int32_t>(pool, pool->geo.error_word), x_early,
+                                   at<int32_t>(pool, pool->geo.error_word), x_early, e4m3,
                                    static_cast<cudaStream_t>(stream), &pool->launches));
 }
 
@@ -264,11 +294,15 @@ int dispatch_call(moe_pool* pool, const uint16_t* x, int32_t T, int buf, bool x_
 extern "C" {
 
 MOE_API int moe_dispatch(moe_pool* pool, const uint16_t* x, int32_t T, int buf, void* stream) {
-    return dispatch_call(pool, x, T, buf, false, stream);
+    return dispatch_call(pool, x, T, buf, false, false, stream);
 }
 
 MOE_API int moe_dispatch_after_plan(moe_pool* pool, const uint16_t* x, int32_t T, int buf, void* stream) {
-    return dispatch_call(pool, x, T, buf, true, stream);
+    return dispatch_call(pool, x, T, buf, true, false, stream);
+}
+
+MOE_API int moe_dispatch_f8(moe_pool* pool, const uint16_t* x, int32_t T, int buf, void* stream) {
+    return dispatch_call(pool, x, T, buf, false, true, stream);
 }
 
 MOE_API int moe_plan_dispatch(moe_pool* pool, const float* logits, int32_t T, const int32_t* rep_off,
@@ -282,13 +316,13 @@ MOE_API int moe_plan_dispatch(moe_pool* pool, const float* logits, int32_t T, co
     if ((rc = moe_plan(pool, logits, T, rep_off, rep_ids, buf, stream)) != MOE_OK) return rc;
     // The plan is the kernel just before, so the dispatch may load x while it
     // runs: x was written before the plan in stream order.
-    return dispatch_call(pool, x, T, buf, true, stream);
+    return dispatch_call(pool, x, T, buf, true, false, stream);
 }
 
 MOE_API int moe_identity_experts(moe_pool* pool, int32_t T, int buf, void* stream) {
     int rc = check_call(pool, T, buf);
     if (rc != MOE_OK) return rc;
-    if (pool->planned_T[buf] != T) return MOE_ERR_STATE;
+    if (pool->planned_T[buf] != T || pool->e4m3[buf]) return MOE_ERR_STATE;
     if (T == 0) return MOE_OK;
     const moe_desc& d = pool->geo.d;
     const SetLayout& L = pool->geo.set[buf];
@@ -356,7 +390,7 @@ MOE_API const char* moe_status_str(int status) {
         case MOE_ERR_CUDA: return "CUDA runtime call failed";
         case MOE_ERR_DEVICE: return "kernel reported a bad index (device error word)";
         case MOE_ERR_REPLICA: return "malformed replica map";
-        case MOE_ERR_STATE: return "T differs from the T planned for this buffer set";
+        case MOE_ERR_STATE: return "T differs from the T planned for this buffer set, or its codes are of another type";
         default: return "unknown status";
     }
 }

@@ -1,7 +1,7 @@
 // route.cuh -- routing of one 32-token tile: the body every plan kernel
 // runs per CTA (top-k by segment arg-max, gates from float pairs, replica
 // pick, per-expert token masks, tile counts and in-tile ranks), with its key
-// mapping and lane helpers.  Included once, by plan.cu, after the trace
+// mapping and lane helpers.  Included by plan_kernels.cuh, after the trace
 // buffers tr_route and tr_single are defined.
 #pragma once
 
@@ -138,6 +138,207 @@ __device__ __forceinline__ float tile_gate(int T, int k, int t0, const float* se
     return g;
 }
 
+// moe_plan's router: keys are the logits, gates the softmax over the k
+// selected ones (tile_gate).
+struct TopkSoftmax {
+    static constexpr bool kScored = false;
+    static bool whole_warps() { return false; }
+};
+
+// moe_plan_routed's router.  Every quantity is binary32:
+//   score s_e = 1 / (1 + exp(-l_e)), or exp(l_e - max l) / sum exp(l - max l)
+//   choice c_e = s_e + bias_e; a group's score is the sum of its group_top
+//   largest choices; the topk_group best groups stay (equal scores: the lower
+//   group); the k largest choices in them are taken (equal: the lower id);
+//   gate = s_e, over the sum of the k selected scores if renorm, times scale.
+// The softmax's sum is carried as a pair of floats, so it does not depend on
+// the order of its terms: the choices, and with them every integer the plan
+// writes, are functions of the inputs alone, whatever the lanes per token.
+struct ScoreRouter {
+    static constexpr bool kScored = true;
+    const float* bias;  // [E] or NULL
+    float scale;
+    bool sigmoid;
+    int n_group, topk_group, group_top;
+    bool renorm;
+    // Groups are compared across a whole warp (one lane per group).
+    bool whole_warps() const { return n_group > 1; }
+
+    // NaN (a NaN logit, or a row without a finite logit) counts as score 0.
+    __device__ __forceinline__ float score(float l, float2 stat) const {
+        const float s = sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - stat.x) / stat.y;
+        return s == s ? s : 0.0f;
+    }
+};
+
+// Keep the keys of the topk_group best groups and clear the others.  Lane
+// `lane` of the whole warp holds the keys of experts [e0, e0 + st).
+template <int EPL>
+__device__ __forceinline__ void keep_best_groups(const ScoreRouter& ro, int E, int e0, int st, int lane,
+                                                 uint32_t (&key)[EPL]) {
+    const int size = E / ro.n_group;
+    const int span = size / st;  // lanes per group
+    if (span * st == size && (span & (span - 1)) == 0) {
+        // Groups fall on whole lanes, a power of two of them (256 experts in 8
+        // groups: 4 lanes each): all groups' two largest at once by a
+        // butterfly over the group's lanes.
+        uint32_t k1, k2;
+        int r1, r2;
+        lane_top2(key, 0u, k1, r1, k2, r2);
+        for (int off = 1; off < span; off <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(kFull, k1, off);
+            const uint32_t o2 = __shfl_xor_sync(kFull, k2, off);
+            k2 = max(min(k1, o1), max(k2, o2));
+            k1 = max(k1, o1);
+        }
+        float v = key_value(k1);
+        if (ro.group_top == 2) v += key_value(k2);
+        const uint32_t mine = order_key(v);
+        const int g = lane / span;
+        int better = 0;
+        for (int q = 0; q < ro.n_group; ++q) {
+            const uint32_t o = __shfl_sync(kFull, mine, q * span);
+            better += (o > mine || (o == mine && q < g)) ? 1 : 0;
+        }
+        if (better >= ro.topk_group) {
+#pragma unroll
+            for (int r = 0; r < EPL; ++r) key[r] = 0u;
+        }
+        return;
+    }
+    // Any other grouping: one group after the other, its largest keys by two
+    // warp reductions; lane q keeps group q's score.
+    uint32_t mine = 0u;
+    for (int q = 0; q < ro.n_group; ++q) {
+        uint32_t in[EPL];
+#pragma unroll
+        for (int r = 0; r < EPL; ++r) {
+            const int e = e0 + r;
+            in[r] = (e >= q * size && e < (q + 1) * size) ? key[r] : 0u;
+        }
+        uint32_t k1, k2;
+        int r1, r2;
+        lane_top2(in, 0u, k1, r1, k2, r2);
+        const uint32_t m1 = __reduce_max_sync(kFull, k1);
+        const int first = __ffs(__ballot_sync(kFull, k1 == m1)) - 1;
+        const uint32_t m2 = __reduce_max_sync(kFull, lane == first ? k2 : k1);
+        float v = key_value(m1);
+        if (ro.group_top == 2) v += key_value(m2);
+        if (lane == q) mine = order_key(v);
+    }
+    int better = 0;
+    for (int q = 0; q < ro.n_group; ++q) {
+        const uint32_t o = __shfl_sync(kFull, mine, q);
+        better += (o > mine || (o == mine && q < lane)) ? 1 : 0;
+    }
+    const unsigned kept = __ballot_sync(kFull, lane < ro.n_group && better < ro.topk_group);
+#pragma unroll
+    for (int r = 0; r < EPL; ++r)
+        if (e0 + r < E && !((kept >> ((e0 + r) / size)) & 1u)) key[r] = 0u;
+}
+
+// The keys of a scored router: the order keys of the choices of experts
+// [e0, e0 + st) of one token (0 past E and for a token past T), groups
+// applied.  A segment of L lanes holds a token; every lane of the warp takes
+// part.  stat gets the softmax's (max, sum).
+template <int EPL, int L>
+__device__ __forceinline__ void scored_keys(const ScoreRouter& ro, const float* __restrict__ row, bool tok_ok, int E,
+                                            int e0, int st, int sl, uint32_t (&key)[EPL], float2* stat) {
+    float v[EPL];
+    const bool quads = ((st | E) & 3) == 0;  // 16-byte aligned runs of four
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) v[r] = -INFINITY;
+    if (tok_ok) {
+        if (EPL >= 4 && quads) {
+#pragma unroll
+            for (int r = 0; r + 3 < EPL; r += 4) {
+                if (r < st && e0 + r < E) {
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(row + e0 + r));
+                    v[r] = q.x;
+                    v[r + 1] = q.y;
+                    v[r + 2] = q.z;
+                    v[r + 3] = q.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < EPL; ++r)
+                if (r < st && e0 + r < E) v[r] = __ldg(row + e0 + r);
+        }
+    }
+    float2 ms = make_float2(0.0f, 1.0f);
+    if (!ro.sigmoid) {
+        float m = v[0];
+#pragma unroll
+        for (int r = 1; r < EPL; ++r) m = fmaxf(m, v[r]);
+#pragma unroll
+        for (int off = 1; off < L; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+        dword::dw sum = {0.0f, 0.0f};
+#pragma unroll
+        for (int r = 0; r < EPL; ++r) {
+            float e = (r < st && e0 + r < E) ? expf(v[r] - m) : 0.0f;
+            if (!(e == e)) e = 0.0f;  // a NaN logit, or no finite one
+            const dword::dw t = dword::two_sum(sum.h, e);
+            sum = dword::fast_two_sum(t.h, sum.l + t.l);
+        }
+#pragma unroll
+        for (int off = 1; off < L; off <<= 1)
+            sum = dword::dw_add(sum, dword::dw{__shfl_xor_sync(kFull, sum.h, off), __shfl_xor_sync(kFull, sum.l, off)});
+        ms = make_float2(m, sum.h);
+    }
+    if (sl == 0) *stat = ms;
+#pragma unroll
+    for (int r = 0; r < EPL; ++r) {
+        const int e = e0 + r;
+        key[r] = 0u;
+        if (tok_ok && r < st && e < E) {
+            float c = ro.score(v[r], ms);
+            if (ro.bias != nullptr) c += __ldg(ro.bias + e);
+            key[r] = order_key(c == c ? c : -INFINITY);
+        }
+    }
+    if (L == 32 && ro.n_group > 1) keep_best_groups(ro, E, e0, st, sl, key);
+}
+
+// The gate of this thread's item, from a scored router: the item's score
+// (without a bias it is the selected choice itself), renormalised over the
+// token's k items by a butterfly over their lanes.  Warp-collective in the
+// first TT kp threads (whole warps).
+template <int TT>
+__device__ __forceinline__ float scored_gate(const ScoreRouter& ro, const float* __restrict__ logits, int T, int E,
+                                             int k, int t0, const float* sel_v, const int32_t* sel_e,
+                                             const float2* stat) {
+    const int kp = k <= 1 ? 1 : 1 << (32 - __clz(k - 1));
+    const int itl = (int)threadIdx.x / kp;
+    const int ij = (int)threadIdx.x - itl * kp;
+    const int it = itl * k + ij;
+    float g = 0.0f;
+    if (((int)threadIdx.x & ~31) < TT * kp) {
+        if (itl < TT && ij < k && t0 + itl < T)
+            g = ro.bias != nullptr ? ro.score(__ldg(logits + (size_t)(t0 + itl) * E + sel_e[it]), stat[itl])
+                                   : sel_v[it];
+        if (ro.renorm) {
+            float sum = g;
+            for (int off = 1; off < kp; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+            g = sum > 0.0f ? g / sum : 0.0f;
+        }
+        g *= ro.scale;
+    }
+    return g;
+}
+
+// The gate of this thread's item for either router.  `head` is the start of
+// the tile's shared memory: the exp table, or the scored router's (max, sum)
+// per token.
+template <int WHERE, int TT, class R>
+__device__ __forceinline__ float router_gate(const R& router, const float* __restrict__ logits, int T, int E, int k,
+                                             int t0, const float* sel_v, const int32_t* sel_e, const float2* head) {
+    if constexpr (R::kScored)
+        return scored_gate<TT>(router, logits, T, E, k, t0, sel_v, sel_e, head);
+    else
+        return tile_gate<WHERE, TT>(T, k, t0, sel_v, head);
+}
+
 // Route one tile of TT tokens (the body every plan kernel runs per CTA) with
 // a CTA of THREADS = TT L threads: each token's top-k runs on a segment of L
 // lanes (L = 32: a whole warp; 16 or 8 when the experts fit in at most 8 keys
@@ -146,8 +347,8 @@ __device__ __forceinline__ float tile_gate(int T, int k, int t0, const float* se
 // spreads a small batch over more SMs with tiles of 8 or 16 tokens.
 // Trace stages: 0 start, 1 top-k done, 2 gates from pairs done, 3 fp64
 // fallback done, 4 replicas and masks done, 5 tile counts and ranks written.
-template <int EPL, int WHERE, int THREADS, int TT = kTileTokens>  // EPL = logits per lane = ceil(E / L)
-__device__ __forceinline__ void route_tile(const float* __restrict__ logits, int T, int E, int P, int k,
+template <int EPL, int WHERE, int THREADS, int TT, class R>  // EPL = logits per lane, at least ceil(E / L)
+__device__ __forceinline__ void route_tile(const R& router, const float* __restrict__ logits, int T, int E, int P, int k,
                                            const int32_t* __restrict__ rep_off,
                                            const int32_t* __restrict__ rep_ids, int32_t* __restrict__ topk_e,
                                            float* __restrict__ gates, int32_t* __restrict__ phys,
@@ -169,8 +370,10 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
     // The exp table and the replica map go to shared memory by asynchronous
     // copies (no registers held, no wait) while the logits are loaded; they
     // are waited for before the barrier that ends the top-k.
-    for (int i = threadIdx.x; i <= 2 * dword::kExpTableHalf; i += THREADS)
-        cp_async8(s_exp + i, dword::kExpTable + i);
+    if (!R::kScored) {
+        for (int i = threadIdx.x; i <= 2 * dword::kExpTableHalf; i += THREADS)
+            cp_async8(s_exp + i, dword::kExpTable + i);
+    }
     if (rep_off != nullptr) {
         for (int i = threadIdx.x; i <= E; i += THREADS) cp_async4(s_off + i, rep_off + i);
         for (int i = threadIdx.x; i < P; i += THREADS) cp_async4(s_ids + i, rep_ids + i);
@@ -181,9 +384,11 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
     const int t = t0 + tl;
 
     // ---- top-k of token t: k rounds of segment arg-max, ties -> lower id ----
-    // Logits become order-preserving unsigned keys (-0 folded onto +0 so that
-    // equal floats give equal keys); lane s of the segment holds experts
-    // s, s + L, s + 2L, ...  Each lane caches its two largest keys; a round
+    // Logits (or a scored router's choices) become order-preserving unsigned
+    // keys (-0 folded onto +0 so that equal floats give equal keys); lane s of
+    // the segment holds experts s, s + L, s + 2L, ...; for a scored router
+    // the run of st = ceil(E / L) experts from s st, so that a group of experts
+    // is a run of lanes.  Each lane caches its two largest keys; a round
     // is one max-reduction of the lanes' first keys over the segment and one
     // min-reduction of the expert id among the lanes holding the maximum,
     // after which the winning lane marks the slot taken and promotes its
@@ -196,15 +401,23 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
         const bool tok_ok = t < T;
         const float* row = logits + (size_t)(tok_ok ? t : t0) * E;
         uint32_t key[EPL];
+        // expert of slot r: first + r * step
+        const int step = R::kScored ? 1 : L;
+        const int held = R::kScored ? (E + L - 1) / L : 0;
+        const int first = R::kScored ? sl * held : sl;
+        if constexpr (R::kScored) {
+            scored_keys<EPL, L>(router, row, tok_ok, E, first, held, sl, key, s_exp + tl);
+        } else {
 #pragma unroll
-        for (int r = 0; r < EPL; ++r) {
-            const int e = r * L + sl;
-            key[r] = (tok_ok && e < E) ? order_key(__ldg(row + e)) : 0u;
+            for (int r = 0; r < EPL; ++r) {
+                const int e = r * L + sl;
+                key[r] = (tok_ok && e < E) ? order_key(__ldg(row + e)) : 0u;
+            }
         }
         uint32_t taken = 0u, k1, k2;
         int r1, r2;
         lane_top2(key, taken, k1, r1, k2, r2);
-        uint32_t cand = (uint32_t)(r1 * L + sl);
+        uint32_t cand = (uint32_t)(first + r1 * step);
         int my_e = 0;
         uint32_t my_key = 0u;
         for (int j = 0; j < k; ++j) {
@@ -227,7 +440,7 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
                 win = (int)(0xffffffffu - (uint32_t)kv);
             }
             if (win >= E) win = 0;  // only reachable with NaN logits (outside the domain)
-            if (sl == (win & (L - 1))) {
+            if (R::kScored ? (unsigned)(win - first) < (unsigned)held : sl == (win & (L - 1))) {
                 taken |= 1u << r1;
                 if (k2 != 0u) {
                     k1 = k2;
@@ -236,7 +449,7 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
                 } else {
                     lane_top2(key, taken, k1, r1, k2, r2);
                 }
-                cand = (uint32_t)(r1 * L + sl);
+                cand = (uint32_t)(first + r1 * step);
             }
             if (sl == j) {
                 my_e = win;
@@ -261,7 +474,7 @@ __device__ __forceinline__ void route_tile(const float* __restrict__ logits, int
     // The cluster plan computes the gates after its cluster barrier's arrive
     // (tile_gate there), where they hide behind the wait for the other CTAs.
     float g = 0.0f;
-    if (WHERE != kRouteInCluster) g = tile_gate<WHERE, TT>(T, k, t0, sel_v, s_exp);
+    if (WHERE != kRouteInCluster) g = router_gate<WHERE, TT>(router, logits, T, E, k, t0, sel_v, sel_e, s_exp);
     if (item_ok) {
         const int tt = t0 + itl;
         const int e = sel_e[it];

@@ -22,7 +22,8 @@ MOE_OK = 0
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SIZE", -3: "MOE_ERR_ALIGN", -4: "MOE_ERR_BUF",
           -5: "MOE_ERR_WORKSPACE", -6: "MOE_ERR_CUDA", -7: "MOE_ERR_DEVICE", -8: "MOE_ERR_REPLICA",
           -9: "MOE_ERR_STATE"}
-DEVERR_REPLICA, DEVERR_DUPLICATE, DEVERR_SLOT = 0x1, 0x2, 0x4
+DEVERR_REPLICA, DEVERR_DUPLICATE, DEVERR_SLOT, DEVERR_WINDOW, DEVERR_STALL = 0x1, 0x2, 0x4, 0x8, 0x10
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class LibraryMissing(ImportError):
@@ -43,6 +44,26 @@ class View(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "ex_out", "topk_e", "phys", "gates", "slot",
                                               "src_token", "src_k", "counts", "offsets", "error_word")] + \
                [("rows", ctypes.c_int32), ("scale_stride", ctypes.c_int32)]
+
+
+class Router(ctypes.Structure):
+    """The scored router of ``Pool.plan_routed`` (moe_router in include/moe.h):
+    ``score`` "sigmoid" or "softmax"; ``topk_group`` of ``n_group`` expert groups
+    are kept by the sum of their ``group_top`` best choices; gates are
+    renormalised over the k chosen scores if ``renorm`` and multiplied by
+    ``scale``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_group", "topk_group", "group_top", "renorm")] + \
+               [("scale", ctypes.c_float)]
+
+    def __init__(self, score="sigmoid", n_group=1, topk_group=1, group_top=1, renorm=True, scale=1.0):
+        if score not in SCORES:
+            raise ValueError(f"score must be one of {sorted(SCORES)}")
+        super().__init__(SCORES[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
+
+
+class ExpertWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("P", "H", "I")] + \
+               [(n, ctypes.c_void_p) for n in ("w13", "s13", "w2", "s2", "error_word")]
 
 
 _lib = None
@@ -76,6 +97,10 @@ def lib() -> ctypes.CDLL:
         "moe_pool_launches": [vp, pp(ctypes.c_uint64)],
         "moe_replica_check": [vp, vp, i32, i32],
         "moe_plan": [vp, vp, i32, vp, vp, ctypes.c_int, vp],
+        "moe_plan_routed": [vp, pp(Router), vp, vp, i32, vp, vp, ctypes.c_int, vp],
+        "moe_dispatch_f8": [vp, vp, i32, ctypes.c_int, vp],
+        "moe_experts_up": [pp(ExpertWeights), vp, vp, i32, vp, i32, vp, vp, i32, vp],
+        "moe_experts_down": [pp(ExpertWeights), vp, vp, i32, vp, i32, vp, vp],
         "moe_dispatch": [vp, vp, i32, ctypes.c_int, vp],
         "moe_dispatch_after_plan": [vp, vp, i32, ctypes.c_int, vp],
         "moe_plan_dispatch": [vp, vp, i32, vp, vp, vp, ctypes.c_int, vp],
@@ -172,6 +197,7 @@ class Pool:
 
         return {
             "codes": t(v.codes, torch.int8, (R, H)),
+            "codes_f8": t(v.codes, torch.float8_e4m3fn, (R, H)),  # the same bytes after dispatch_f8
             "scales": t(v.scales, torch.float32, (R, v.scale_stride)),
             "ex_out": t(v.ex_out, torch.bfloat16, (R, H)),
             "topk_e": t(v.topk_e, torch.int32, (T, k)),
@@ -190,6 +216,26 @@ class Pool:
         T = logits.shape[0]
         _call("moe_plan", self.handle, _ptr(logits), T, _ptr(rep_off), _ptr(rep_ids), buf, _stream(stream))
         return T
+
+    def plan_routed(self, logits, router, bias=None, rep_off=None, rep_ids=None, buf=0, stream=None):
+        """moe_plan_routed: the plan with a scored router (a ``Router``);
+        ``bias`` fp32 [E] is added to the scores for the choice only."""
+        T = logits.shape[0]
+        _call("moe_plan_routed", self.handle, ctypes.byref(router), _ptr(logits), _ptr(bias), T, _ptr(rep_off),
+              _ptr(rep_ids), buf, _stream(stream))
+        return T
+
+    def dispatch_f8(self, x, buf=0, stream=None):
+        """moe_dispatch_f8: dispatch with E4M3 codes (view()["codes_f8"])."""
+        _call("moe_dispatch_f8", self.handle, _ptr(x), x.shape[0], buf, _stream(stream))
+
+    def experts(self, experts, T, h, h_scales, buf=0, stream=None):
+        """The set's rows (after ``dispatch_f8``) through ``experts``: their
+        gated product into ``h`` / ``h_scales`` (``Experts.inner(rows)``), then
+        their down projection into the set's ex_out, ready for ``combine``."""
+        v, n = self.view(buf), T * self.k
+        experts.up(v["codes_f8"][:n], v["scales"][:n], v["offsets"], h, h_scales, stream=stream)
+        experts.down(h[:n], h_scales[:n], v["offsets"], v["ex_out"][:n], stream=stream)
 
     def dispatch(self, x, buf=0, stream=None, after_plan=False):
         """moe_dispatch; with ``after_plan`` moe_dispatch_after_plan, which
@@ -260,3 +306,74 @@ def plan_static(logits, k, P=None, rep_off=None, rep_ids=None, out=None, stream=
           *[_ptr(out[n]) for n in ("topk_e", "gates", "phys", "counts", "offsets", "slot", "src_token", "src_k",
                                     "error_word")], _stream(stream))
     return out
+
+
+class Experts:
+    """The weights of P gated feed-forward experts, E4M3 with one fp32 scale
+    per 128 x 128 block, and their products over expert windows (moe_experts_up,
+    moe_experts_down).
+
+    w13 [P, 2 I, H] (gate rows, then up rows) with s13 [P, 2 I / 128, H / 128],
+    w2 [P, H, I] with s2 [P, H / 128, I / 128]; either pair may be left out, and
+    with it its product.  ``check()`` returns the device error word."""
+
+    def __init__(self, w13=None, s13=None, w2=None, s2=None):
+        if (w13 is None) != (s13 is None) or (w2 is None) != (s2 is None) or (w13 is None and w2 is None):
+            raise ValueError("give w13 and s13, w2 and s2, or both pairs")
+        if w13 is not None:
+            self.P, self.I, self.H = w13.shape[0], w13.shape[1] // 2, w13.shape[2]
+        else:
+            self.P, self.H, self.I = w2.shape
+        P, H, I = self.P, self.H, self.I
+        for name, w, s, n, k in (("w13", w13, s13, 2 * I, H), ("w2", w2, s2, H, I)):
+            if w is not None:
+                _tensor(name, w, torch.float8_e4m3fn, (P, n, k))
+                _tensor("s" + name[1:], s, torch.float32, (P, n // 128, k // 128))
+        self.w13, self.s13, self.w2, self.s2 = w13, s13, w2, s2
+        device = (w13 if w13 is not None else w2).device
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(device).synchronize()  # zero before any stream's kernels may set it
+        self.weights = ExpertWeights(P, H, I, *[_ptr(t) for t in (w13, s13, w2, s2, self.error_word)])
+
+    def inner(self, rows):
+        """Buffers for ``rows`` rows between the two products: E4M3 [rows, I]
+        and fp32 scales [rows, I / 128 rounded up to 4]."""
+        dev = self.error_word.device
+        return (torch.empty((rows, self.I), dtype=torch.float8_e4m3fn, device=dev),
+                torch.zeros((rows, (self.I // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
+
+    def up(self, codes, scales, offsets, h, h_scales, stream=None):
+        """h, h_scales = quantised silu(rows gate^T) * (rows up^T) per window."""
+        rows = codes.shape[0]
+        _tensor("codes", codes, torch.float8_e4m3fn, (rows, self.H))
+        _tensor("scales", scales, torch.float32, (rows, None))
+        _tensor("offsets", offsets, torch.int32, (self.P + 1,))
+        _tensor("h", h, torch.float8_e4m3fn, (None, self.I), rows)
+        _tensor("h_scales", h_scales, torch.float32, (None, None), rows)
+        _call("moe_experts_up", ctypes.byref(self.weights), _ptr(codes), _ptr(scales), scales.shape[1], _ptr(offsets),
+              rows, _ptr(h), _ptr(h_scales), h_scales.shape[1], _stream(stream))
+        return h, h_scales
+
+    def down(self, h, h_scales, offsets, out, stream=None):
+        """out = bf16(h w2^T) per window."""
+        rows = h.shape[0]
+        _tensor("h", h, torch.float8_e4m3fn, (rows, self.I))
+        _tensor("h_scales", h_scales, torch.float32, (rows, None))
+        _tensor("offsets", offsets, torch.int32, (self.P + 1,))
+        _tensor("out", out, torch.bfloat16, (None, self.H), rows)
+        _call("moe_experts_down", ctypes.byref(self.weights), _ptr(h), _ptr(h_scales), h_scales.shape[1],
+              _ptr(offsets), rows, _ptr(out), _stream(stream))
+        return out
+
+    def check(self, stream=None) -> int:
+        """Wait for ``stream`` and return the device error word (0 = clean)."""
+        (stream or torch.cuda.current_stream()).synchronize()
+        return int(self.error_word.item())
+
+
+def _tensor(name, t, dtype, shape, least=0):
+    """A dense tensor of this type and shape (None: any size), with at least
+    ``least`` rows."""
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or t.shape[0] < least or \
+            any(want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")

@@ -15,14 +15,18 @@
  *                 generation and token reordering before dispatch",
  *                 write-up section "Prefill Phase"; expert-window aggregation,
  *                 StrataCL analysis section 3.5).
+ *                 moe_plan_routed: the same with a scored router (sigmoid or
+ *                 softmax scores, balance bias, expert groups).
  *   moe_dispatch  fused per-token INT8 quantization (one fp32 scale per 128
  *                 elements) and scatter of each token into its k slots
  *                 (write-up: "Early INT8 Quantization", "AIV-Direct Write",
  *                 "Token-Level Pipeline").
  *   moe_plan_dispatch  both in one call; the dispatch then reads x while
  *                 the plan runs, safely.
- *   (experts)     outside this library; moe_identity_experts is a stand-in
- *                 that dequantizes each slot row (code * scale -> bf16).
+ *   (experts)     moe_experts_up and moe_experts_down on rows dispatched by
+ *                 moe_dispatch_f8, or the caller's own; moe_identity_experts is
+ *                 a stand-in that dequantizes each INT8 slot row (code * scale
+ *                 -> bf16).
  *   moe_combine   gate-weighted gather-reduce of the k bf16 expert rows back
  *                 to token order, fp32 fma in ascending j (write-up: "expert
  *                 output return").
@@ -77,13 +81,16 @@ typedef enum moe_status {
     MOE_ERR_CUDA = -6,      /* a CUDA runtime call failed */
     MOE_ERR_DEVICE = -7,    /* a kernel reported a bad index (error word) */
     MOE_ERR_REPLICA = -8,   /* malformed replica map (host check) */
-    MOE_ERR_STATE = -9      /* T differs from the one planned for this set */
+    MOE_ERR_STATE = -9      /* T differs from the one planned for this set, or its
+                               codes are of another type than the call reads */
 } moe_status;
 
 /* Device error-word bits (moe_pool_check). */
 #define MOE_DEVERR_REPLICA 0x1   /* replica map gave an id outside [0, P) */
 #define MOE_DEVERR_DUPLICATE 0x2 /* a token mapped twice to one physical expert */
 #define MOE_DEVERR_SLOT 0x4      /* a slot index outside [0, T*k) */
+#define MOE_DEVERR_WINDOW 0x8    /* an expert window outside the rows (moe_experts_*) */
+#define MOE_DEVERR_STALL 0x10    /* a wait inside moe_experts_* ran out */
 
 /*
  * Pool geometry, fixed at init (static pre-allocation: write-up,
@@ -214,6 +221,45 @@ MOE_API int moe_plan(moe_pool* pool, const float* logits, int32_t T,
                      const int32_t* rep_off, const int32_t* rep_ids, int buf, void* stream);
 
 /*
+ * The scored router of moe_plan_routed.  Everything is computed in binary32.
+ *   score       MOE_SCORE_SIGMOID: s_e = 1 / (1 + exp(-l_e)), or
+ *               MOE_SCORE_SOFTMAX: s_e = exp(l_e - max l) / sum exp(l - max l)
+ *               over all E experts (the sum carried in two floats)
+ *   n_group     groups of E / n_group consecutive experts, 1 .. 32, a divisor
+ *               of E; 1 = no groups
+ *   topk_group  groups a token may choose from, 1 .. n_group, holding at
+ *               least k experts
+ *   group_top   a group's score is the sum of its 1 or 2 largest choices
+ *   renorm      nonzero: a token's gates are divided by the sum of its k scores
+ *   scale       factor on the gates, finite and > 0
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct moe_router {
+    int32_t score, n_group, topk_group, group_top, renorm;
+    float scale;
+} moe_router;
+
+/*
+ * moe_plan_routed: moe_plan with a scored router (the routing metadata of one
+ * layer, for models whose router is not a softmax over the k largest logits).
+ *   bias  device fp32 [E] added to the scores for the choice only (load
+ *         balance without an auxiliary loss), or NULL
+ * Per token: choice c_e = s_e + bias_e; the topk_group groups with the largest
+ * group scores (equal: the lower group); among their experts the k largest
+ * choices, in that order (equal: the lower expert id); gate = s_e (over the sum
+ * of the token's k scores with renorm; 0 if that sum is 0) times scale.  From
+ * there on as moe_plan: replica pick, counts, offsets, slots, inverse maps,
+ * the same kernels and forms, and the same arguments and errors; a router
+ * outside the ranges above is MOE_ERR_SIZE.  A logit of -inf has score 0, and
+ * so has a NaN; a token whose logits are all -inf takes the lowest ids of the
+ * first groups with gates 0 (softmax).  A bias of -inf keeps an expert from
+ * being chosen while the allowed groups hold k others.
+ */
+MOE_API int moe_plan_routed(moe_pool* pool, const moe_router* router, const float* logits, const float* bias,
+                            int32_t T, const int32_t* rep_off, const int32_t* rep_ids, int buf, void* stream);
+
+/*
  * moe_dispatch: quantize x and scatter into the set's dispatch rows
  * (write-up, "FusedDispatch and FusedCombine": "Early INT8 Quantization",
  * "AIV-Direct Write", "Token-Level Pipeline").
@@ -225,6 +271,20 @@ MOE_API int moe_plan(moe_pool* pool, const float* logits, int32_t T,
  * x may be written by anything earlier on `stream`, kernels included.
  */
 MOE_API int moe_dispatch(moe_pool* pool, const uint16_t* x, int32_t T, int buf, void* stream);
+
+/*
+ * moe_dispatch_f8: moe_dispatch with codes in 8-bit floating point (E4M3:
+ * 4 exponent bits, 3 fraction bits, largest value 448), the operand type of
+ * moe_experts_up ("Early INT8 Quantization", for experts whose products run on
+ * the 8-bit floating-point tensor pipe).  Per token and 128-element group:
+ * amax = max |x|, scale = amax / 448 (fp32), code = (x * 448) / amax, the
+ * correctly rounded fp32 quotient, rounded to the nearest E4M3 value, ties to
+ * even (amax = 0: scale 0, codes 0).  The same buffers, layout, arguments and
+ * errors as moe_dispatch: codes holds E4M3 bytes, and moe_identity_experts,
+ * which reads INT8, returns MOE_ERR_STATE until the set is dispatched in INT8
+ * again.
+ */
+MOE_API int moe_dispatch_f8(moe_pool* pool, const uint16_t* x, int32_t T, int buf, void* stream);
 
 /*
  * moe_dispatch_after_plan: moe_dispatch for the plan -> dispatch sequence,
@@ -256,6 +316,60 @@ MOE_API int moe_dispatch_after_plan(moe_pool* pool, const uint16_t* x, int32_t T
  */
 MOE_API int moe_plan_dispatch(moe_pool* pool, const float* logits, int32_t T, const int32_t* rep_off,
                               const int32_t* rep_ids, const uint16_t* x, int buf, void* stream);
+
+/*
+ * The experts' weights: one gated feed-forward network per physical expert,
+ * in E4M3 with one fp32 scale per 128 x 128 block.  A plain struct of device
+ * pointers, kept and filled by the caller; every pointer 16-byte aligned.
+ *   P, H, I   physical experts 1 .. 4096; hidden and inner size, multiples of
+ *             128, 128 .. 65536
+ *   w13, s13  [P, 2 I, H] E4M3 and [P, 2 I / 128, H / 128] fp32: rows 0 .. I-1
+ *             the gate projection, rows I .. 2I-1 the up projection
+ *   w2, s2    [P, H, I] E4M3 and [P, H / 128, I / 128] fp32: down projection
+ *   error_word device int32 [1]; error bits are OR-ed in (zero it first)
+ * moe_experts_up needs w13 / s13 only, moe_experts_down w2 / s2 only.
+ */
+typedef struct moe_experts {
+    int32_t P, H, I;
+    const uint8_t* w13;
+    const float* s13;
+    const uint8_t* w2;
+    const float* s2;
+    int32_t* error_word;
+} moe_experts;
+
+/*
+ * moe_experts_up: the experts' first products, their gated activation and its
+ * quantization, for every row of every expert window, in one kernel:
+ *   g, u = rows * gate^T, rows * up^T       h = g / (1 + exp(-g)) * u
+ *   codes [rows, H] E4M3, scales [rows, scale_stride] fp32 per 128 elements:
+ *            dispatched rows (a set's codes and scales after moe_dispatch_f8,
+ *            or a receive buffer in that layout)
+ *   offsets  device int32 [P + 1]: expert p's window is rows offsets[p] ..
+ *            offsets[p + 1] - 1 (a set's offsets)
+ *   rows     rows in the buffers; windows must lie inside [0, rows)
+ *   h [rows, I] E4M3, h_scales [rows, h_stride] fp32 out: per row and 128
+ *            columns scale = max |h| / 448 and code = h * (448 / max |h|) rounded
+ *            to nearest even (all zero: scale 0, codes 0)
+ * Products of codes are summed in fp32 over each 128-element block on the
+ * tensor cores, scaled by row scale x weight scale, and added up in fp32.
+ * scale_stride, h_stride: multiples of 4 holding H / 128 and I / 128 groups.
+ * A window outside the rows is skipped and sets MOE_DEVERR_WINDOW; rows of no
+ * window are left as they are.  rows = 0: no-op.
+ */
+MOE_API int moe_experts_up(const moe_experts* experts, const uint8_t* codes, const float* scales,
+                           int32_t scale_stride, const int32_t* offsets, int32_t rows, uint8_t* h, float* h_scales,
+                           int32_t h_stride, void* stream);
+
+/*
+ * moe_experts_down: out[r] = bf16(h[r] * w2[p]^T) for every row r of every
+ * expert window p, the rows moe_combine reads ("expert output return").
+ *   h, h_scales, h_stride, offsets, rows   as moe_experts_up
+ *   out  bf16 [rows, H] (a set's ex_out)
+ * Sums as in moe_experts_up, rounded once to bf16.
+ */
+MOE_API int moe_experts_down(const moe_experts* experts, const uint8_t* h, const float* h_scales, int32_t h_stride,
+                             const int32_t* offsets, int32_t rows, uint16_t* out, void* stream);
 
 /*
  * Identity experts (test stand-in for the expert FFNs): for rows r < T*k,
