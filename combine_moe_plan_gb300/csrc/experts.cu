@@ -6,96 +6,472 @@
 // 128-element blocks of the inner dimension.  moe_experts_up computes gate and
 // up outputs of the same 128 columns, h = silu(gate) up, and quantizes the 128
 // values of each row as one group; moe_experts_down rounds y to bf16.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+#include <cuda.h>
 
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRowTile = 16;  // rows a CTA accumulates at a time
+constexpr int kTileM = 128;        // rows of a tile (TMEM lanes)
+constexpr int kTileN = 256;        // outputs of a tile: two 128-blocks of weight rows
+constexpr int kStages = 4;         // operand buffers
+constexpr int kRowBox = 32;        // rows per TMA box of the row operand
+constexpr int kABytes = kTileM * kGroup;
+constexpr int kBHalf = kGroup * kGroup;
+constexpr int kStageBytes = kABytes + 2 * kBHalf;
+constexpr int kSumWarps = 8;       // warps that scale and add up
+constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
+constexpr int kExpertsThreads = 32 * (kSumWarps + 4);  // three warpgroups
+// Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
+// 256 x 224 + 128 x 48 = 63,488.
+constexpr int kSumRegs = 224, kOtherRegs = 48;
+constexpr int kHalfN = 64;         // columns of each 128-block that a summing warp owns
 
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+struct Barriers {
+    uint64_t full[kStages], empty[kStages];  // operand buffers
+    uint64_t acc_full[2], acc_empty[2];      // TMEM accumulators of one 128-block of K
+    uint64_t drain;
+    uint32_t tmem;
+    int gave_up;
+    int warp_total[kExpertsThreads / 32], warp_top[kExpertsThreads / 32];
+    float amax[2][2][kTileM];  // [tile parity][column half][row]
+};
+
+struct Problem {
+    int P, N, K;  // experts, outputs per row, inner size
+    const float* sa;
+    int sa_stride;
+    const float* sw;
+    const int32_t* offsets;
+    int rows;
+    uint8_t* h;
+    float* hs;
+    int hs_stride;
+    uint16_t* out;
+    int32_t* err;
+};
+
+// A tile: kTileM rows of one expert's window (from `row`, `valid` of them) by
+// two 128-blocks of its weight rows: UP: gate block n and up block n; down:
+// blocks 2n and 2n + 1 (the last one alone where their number is odd).
+struct Tile {
+    int p, n, row, valid;
+};
+
+// Tiles in the order (expert, n, rows), rows fastest: CTAs working side by
+// side share a block of weights.  first_m[p] counts the row tiles before
+// expert p.  Tile indices only grow, so the expert is found by moving on.
+struct TileWalk {
+    int p = 0;
+    __device__ __forceinline__ Tile at(int tile, int n_tiles, const int* first_m, const int32_t* offsets,
+                                       int P) {
+        const int m_index = tile / n_tiles;
+        while (p + 1 < P && first_m[p + 1] <= m_index) ++p;
+        const int m_tiles = first_m[p + 1] - first_m[p];
+        const int local = tile - first_m[p] * n_tiles;
+        Tile t;
+        t.p = p;
+        t.n = local / m_tiles;
+        const int lo = offsets[p], hi = offsets[p + 1];
+        t.row = lo + (local - t.n * m_tiles) * kTileM;
+        t.valid = min(kTileM, hi - t.row);
+        return t;
+    }
+};
+
+// The largest value of the threads before this one (0 for the first).
+__device__ __forceinline__ int block_max_before(int v, int* warp_top) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl = max(incl, o);
+    }
+    if (lane == 31) warp_top[warp] = incl;
+    int before = __shfl_up_sync(kFull, incl, 1);
+    if (lane == 0) before = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before = max(before, warp_top[w]);
+    return before;
 }
 
-// One CTA per (128 output columns, expert); a thread owns one column (UP: the
-// gate and the up column) of kRowTile rows at a time.
+// First row tile of every expert, in shared memory; returns their number.  A
+// window that leaves the rows, runs backwards or starts before an earlier
+// offset (it could share rows with an earlier window) counts as empty and is
+// reported.
+__device__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, int* warp_top) {
+    const int per = (pr.P + kExpertsThreads - 1) / kExpertsThreads;
+    const int lo = min(pr.P, (int)threadIdx.x * per), hi = min(pr.P, lo + per);
+    // the largest offset before this thread's first
+    int top = 0;
+    for (int p = lo; p < hi; ++p) top = max(top, pr.offsets[p]);
+    top = block_max_before(top, warp_top);
+    int sum = 0;
+    for (int p = lo; p < hi; ++p) {
+        const int a = pr.offsets[p], b = pr.offsets[p + 1];
+        const bool ok = a >= top && b >= a && b <= pr.rows;
+        top = max(top, a);
+        if (!ok && blockIdx.x == 0) set_error(pr.err, MOE_DEVERR_WINDOW);
+        const int m = ok ? (b - a + kTileM - 1) / kTileM : 0;
+        first_m[p] = m;
+        sum += m;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int base = 0, total = 0;
+    for (int w = 0; w < kExpertsThreads / 32; ++w) {
+        if (w < warp) base += warp_total[w];
+        total += warp_total[w];
+    }
+    int run = base + incl - sum;
+    for (int p = lo; p < hi; ++p) {
+        const int m = first_m[p];
+        first_m[p] = run;
+        run += m;
+    }
+    if (threadIdx.x == 0) first_m[pr.P] = total;
+    __syncthreads();
+    return total;
+}
+
+// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e) held as a sum of
+// two floats, so that its relative error stays at the approximations' own
+// (2^-22 each) for every g; where exp overflows the quotient is 0.
+__device__ __forceinline__ float gated(float g, float u) {
+    const float x = fminf(fmaxf(g, -200.0f), 100.0f);  // past these the limits are reached
+    const float t = x * -1.44269504f;
+    const float lo = fmaf(x, -1.44269504f, -t) - x * 1.925963033e-8f;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fminf(fmaf(e, lo * 0.693147181f, e), 3e38f);  // never NaN (fminf)
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
+}
+
 template <bool UP>
-__global__ void __launch_bounds__(kGroup)
-experts_kernel(int P, int N, int K, const uint8_t* __restrict__ a, const float* __restrict__ sa, int sa_stride,
-               const uint8_t* __restrict__ w, const float* __restrict__ sw, const int32_t* __restrict__ offsets,
-               int rows, uint8_t* __restrict__ h, float* __restrict__ hs, int hs_stride, uint16_t* __restrict__ out,
-               int32_t* __restrict__ err) {
-    __shared__ float s_a[kRowTile][kGroup];
-    __shared__ float s_max[kGroup / 32][kRowTile];
+__global__ void __launch_bounds__(kExpertsThreads, 1)
+experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Problem pr) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char* stages = smem + (1024u - (smem_u32(smem) & 1023u)) % 1024u;
+    Barriers& b = *reinterpret_cast<Barriers*>(stages + kStages * kStageBytes);
+    int* first_m = reinterpret_cast<int*>(&b + 1);  // [P + 1]
+    volatile int* gave_up = &b.gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == kMmaWarp) {
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&b.full[s], 1);
+                mbar_init(&b.empty[s], 1);
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(&b.acc_full[s], 1);
+                mbar_init(&b.acc_empty[s], kSumWarps);
+            }
+            mbar_init(&b.drain, 1);
+            b.gave_up = 0;
+            mbar_init_fence();
+        }
+        __syncwarp();
+        tmem_alloc_all(&b.tmem);
+        tc_fence_before();
+    } else if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_w);
+    }
     grid_dependency_sync();
     allow_dependents();
-    const int p = blockIdx.y, nb = blockIdx.x, c = threadIdx.x;
-    const int lo = offsets[p], hi = offsets[p + 1];
-    if (lo < 0 || hi < lo || hi > rows) {
-        if (c == 0) set_error(err, MOE_DEVERR_WINDOW);
-        return;
-    }
-    const int kb = K / kGroup, width = UP ? 2 * N : N;  // N: output columns
-    const int n = nb * kGroup + c;
-    const uint8_t* w0 = w + ((size_t)p * width + n) * K;
-    const uint8_t* w1 = w0 + (size_t)N * K;
-    const float* sw0 = sw + ((size_t)p * (width / kGroup) + nb) * kb;
-    const float* sw1 = sw0 + (size_t)(N / kGroup) * kb;
-    for (int r0 = lo; r0 < hi; r0 += kRowTile) {
-        const int nr = min(kRowTile, hi - r0);
-        float y0[kRowTile], y1[kRowTile];
-#pragma unroll
-        for (int r = 0; r < kRowTile; ++r) y0[r] = y1[r] = 0.0f;
-        for (int b = 0; b < kb; ++b) {
-            __syncthreads();
-            for (int r = 0; r < kRowTile; ++r)
-                s_a[r][c] = r < nr ? e4m3_value(a[(size_t)(r0 + r) * K + b * kGroup + c]) : 0.0f;
-            __syncthreads();
-            float t0[kRowTile], t1[kRowTile];
-#pragma unroll
-            for (int r = 0; r < kRowTile; ++r) t0[r] = t1[r] = 0.0f;
-            for (int i = 0; i < kGroup; ++i) {
-                const float v0 = e4m3_value(w0[b * kGroup + i]);
-                const float v1 = UP ? e4m3_value(w1[b * kGroup + i]) : 0.0f;
-#pragma unroll
-                for (int r = 0; r < kRowTile; ++r) {
-                    t0[r] = fmaf(s_a[r][i], v0, t0[r]);
-                    if (UP) t1[r] = fmaf(s_a[r][i], v1, t1[r]);
+    const int m_total = scan_windows(pr, first_m, b.warp_total, b.warp_top);  // its barriers publish the above
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+
+    const int blocks = pr.N / kGroup;                       // 128-blocks of outputs
+    const int n_tiles = UP ? blocks : (blocks + 1) / 2;
+    const int width = UP ? 2 * pr.N : pr.N;                 // weight rows per expert
+    const int kb = pr.K / kGroup;
+    const long long tiles = (long long)m_total * n_tiles;   // at most 2^31: checked by the host
+    TileWalk walk;
+
+    if (warp >= kSumWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kTmaWarp && lane == 0) {
+            int s = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                const int w0 = t.p * width + (UP ? t.n : 2 * t.n) * kGroup;
+                const bool two = UP || 2 * t.n + 1 < blocks;
+                const int w1 = UP ? w0 + pr.N : w0 + kGroup;
+                const int boxes = (t.valid + kRowBox - 1) / kRowBox;
+                const uint32_t bytes = boxes * kRowBox * kGroup + (two ? 2 : 1) * kBHalf;
+                for (int k = 0; k < kb; ++k) {
+                    if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
+                    unsigned char* a = stages + s * kStageBytes;
+                    mbar_expect_tx(&b.full[s], bytes);
+                    tma_load_2d(a + kABytes, &map_w, k * kGroup, w0, &b.full[s]);
+                    if (two) tma_load_2d(a + kABytes + kBHalf, &map_w, k * kGroup, w1, &b.full[s]);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(a + i * kRowBox * kGroup, &map_a, k * kGroup, t.row + i * kRowBox, &b.full[s]);
+                    ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
+            if (!ok) {  // leave only after the copies in flight have landed (or not at all)
+                set_error(pr.err, MOE_DEVERR_STALL);
+                const uint64_t t0 = now_ns();
+                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                    while (!mbar_try(&b.full[i % kStages], (i / kStages) & 1) && now_ns() - t0 < kStallNs) {
+                    }
+            }
+        }
+        if (warp == kMmaWarp && lane == 0) {
+            int s = 0;
+            uint32_t phase = 0, it = 0;
+            bool ok = true;
+            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                const bool two = UP || 2 * t.n + 1 < blocks;
+                const uint32_t idesc = umma_idesc_e4m3(kTileM, two ? kTileN : kGroup);
+                for (int k = 0; k < kb; ++k, ++it) {
+                    const uint32_t buf = it & 1;
+                    if (!(ok = mbar_wait(&b.acc_empty[buf], ((it >> 1) & 1) ^ 1, gave_up))) break;
+                    if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
+                    tc_fence_after();
+                    const uint64_t da = umma_desc(stages + s * kStageBytes);
+                    const uint64_t dw = umma_desc(stages + s * kStageBytes + kABytes);
 #pragma unroll
-            for (int r = 0; r < kRowTile; ++r) {
-                if (r < nr) {
-                    const float f = sa[(size_t)(r0 + r) * sa_stride + b];
-                    y0[r] = fmaf(f * sw0[b], t0[r], y0[r]);
-                    if (UP) y1[r] = fmaf(f * sw1[b], t1[r], y1[r]);
+                    for (int i = 0; i < kGroup / 32; ++i)
+                        umma_e4m3(tmem + buf * kTileN, da + 2 * i, dw + 2 * i, idesc, i != 0);
+                    umma_commit(&b.empty[s]);
+                    umma_commit(&b.acc_full[buf]);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                set_error(pr.err, MOE_DEVERR_STALL);
+                umma_commit(&b.drain);
+                const uint64_t t0 = now_ns();
+                while (!mbar_try(&b.drain, 0) && now_ns() - t0 < kStallNs) {
                 }
             }
         }
-        if (!UP) {
-            for (int r = 0; r < nr; ++r)
-                out[(size_t)(r0 + r) * N + n] = (uint16_t)(pack_bf16x2_rn(y0[r], 0.0f) & 0xffffu);
-            continue;
-        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        // Summing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
+        // thread) and of each 128-block the columns 64 (w / 4) .. + 63.
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalfN;
+        uint32_t it = 0, parity = 0;
+        bool ok = true;
+        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, parity ^= 1) {
+            const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+            const bool two = UP || 2 * t.n + 1 < blocks;
+            const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
+            const int in_tile = quarter * 32 + lane;
+            const size_t row = (size_t)t.row + min(in_tile, t.valid - 1);
+            const float* sa = pr.sa + row * pr.sa_stride;
+            const int blk = UP ? t.n : 2 * t.n;
+            const float* sw0 = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
+            const float* sw1 = UP ? sw0 + (size_t)blocks * kb : (two ? sw0 + kb : sw0);
+            uint64_t acc[2][kHalfN / 2];
 #pragma unroll
-        for (int r = 0; r < kRowTile; ++r) {
-            y0[r] = y0[r] / (1.0f + expf(-y0[r])) * y1[r];
-            const unsigned m = __reduce_max_sync(kFull, __float_as_uint(fabsf(y0[r])));
-            if ((c & 31) == 0) s_max[c / 32][r] = __uint_as_float(m);
+            for (int i = 0; i < kHalfN / 2; ++i) acc[0][i] = acc[1][i] = 0ull;
+            float4 a4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (busy) a4 = __ldg(reinterpret_cast<const float4*>(sa));
+            float4 next = a4;
+            float f0 = __ldg(sw0), f1 = __ldg(sw1);
+            for (int k = 0; k < kb; ++k, ++it) {
+                const uint32_t buf = it & 1;
+                if ((k & 3) == 0) {
+                    a4 = next;
+                    if (busy && k + 4 < kb) next = __ldg(reinterpret_cast<const float4*>(sa + k + 4));
+                }
+                const float ar = (k & 2) ? ((k & 1) ? a4.w : a4.z) : ((k & 1) ? a4.y : a4.x);
+                const float s0 = ar * f0, s1 = ar * f1;
+                if (k + 1 < kb) {
+                    f0 = __ldg(sw0 + k + 1);
+                    f1 = __ldg(sw1 + k + 1);
+                }
+                if (!(ok = mbar_wait(&b.acc_full[buf], (it >> 1) & 1, gave_up))) break;
+                __syncwarp();
+                tc_fence_after();
+                if (busy) {
+                    const uint64_t s2[2] = {pack2(__float_as_uint(s0), __float_as_uint(s0)),
+                                            pack2(__float_as_uint(s1), __float_as_uint(s1))};
+                    const uint32_t base = my_tmem + buf * kTileN;
+                    uint32_t v[2][16];
+                    tmem_load16(base, v[0]);
+#pragma unroll
+                    for (int c = 0; c < 2 * kHalfN / 16; ++c) {
+                        tmem_wait_load(v[c & 1]);
+                        if (c + 1 < 2 * kHalfN / 16)
+                            tmem_load16(base + ((c + 1) / (kHalfN / 16)) * kGroup + ((c + 1) % (kHalfN / 16)) * 16,
+                                        v[(c + 1) & 1]);
+                        const int blkc = c / (kHalfN / 16), c0 = (c % (kHalfN / 16)) * 8;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[blkc][c0 + i] = fma2(pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2[blkc],
+                                                     acc[blkc][c0 + i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.acc_empty[buf]);
+            }
+            if (!ok) {
+                if (UP) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");  // let the partner go on
+                break;
+            }
+            const bool store = in_tile < t.valid;
+            if constexpr (UP) {
+                float amax = 0.0f;
+                if (busy) {
+#pragma unroll
+                    for (int i = 0; i < kHalfN / 2; ++i) {
+                        const float2 g = unpack2(acc[0][i]), u = unpack2(acc[1][i]);
+                        const float x = gated(g.x, u.x), y = gated(g.y, u.y);
+                        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+                        acc[0][i] = pack2(__float_as_uint(x), __float_as_uint(y));
+                    }
+                }
+                // the row's other 64 columns are with the warp 4 further (or back)
+                b.amax[parity][half][in_tile] = amax;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                amax = fmaxf(amax, b.amax[parity][half ^ 1][in_tile]);
+                if (store) {
+                    // a tiny group is scaled up first, so that 448 / amax stays finite
+                    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+                    const float inv = amax > 0.0f ? kE4M3Max / (amax * lift) : 0.0f;
+                    uint32_t q[kHalfN / 4];
+#pragma unroll
+                    for (int i = 0; i < kHalfN / 4; ++i) {
+                        const float2 x = unpack2(acc[0][2 * i]), y = unpack2(acc[0][2 * i + 1]);
+                        q[i] = pack_e4m3x2(x.x * lift * inv, x.y * lift * inv) |
+                               pack_e4m3x2(y.x * lift * inv, y.y * lift * inv) << 16;
+                    }
+                    uint8_t* dst = pr.h + row * pr.N + (size_t)t.n * kGroup + half * kHalfN;
+#pragma unroll
+                    for (int i = 0; i < kHalfN / 16; ++i)
+                        st16(dst + 16 * i, make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]));
+                    if (half == 0) pr.hs[row * pr.hs_stride + t.n] = amax / kE4M3Max;
+                }
+            } else if (store) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c == 1 && !two) break;
+                    uint16_t* dst = pr.out + row * pr.N + (size_t)(2 * t.n + c) * kGroup + half * kHalfN;
+#pragma unroll
+                    for (int i = 0; i < kHalfN / 8; ++i) {
+                        uint32_t q[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = unpack2(acc[c][4 * i + j]);
+                            q[j] = pack_bf16x2_rn(x.x, x.y);
+                        }
+                        st16(dst + 8 * i, make_uint4(q[0], q[1], q[2], q[3]));
+                    }
+                }
+            }
         }
-        __syncthreads();
-        for (int r = 0; r < nr; ++r) {
-            const float m = fmaxf(fmaxf(s_max[0][r], s_max[1][r]), fmaxf(s_max[2][r], s_max[3][r]));
-            const float den = m > 0.0f ? m : 1.0f;
-            h[(size_t)(r0 + r) * N + n] = (uint8_t)(pack_e4m3x2(y0[r] * kE4M3Max / den, 0.0f) & 0xffu);
-            if (c == 0) hs[(size_t)(r0 + r) * hs_stride + nb] = m / kE4M3Max;
-        }
+        if (!ok && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
+        tc_fence_before();
     }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ---- host side ----
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime (no driver library is linked);
+// NULL if there is none.  Looked up once.
+EncodeTiledFn encode_tiled() {
+    static const EncodeTiledFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+
+// A map of [rows, K] bytes in boxes of box_rows x 128 bytes, 128-byte swizzle;
+// rows past the end read as zero.
+bool byte_map(CUtensorMap* m, const void* base, size_t rows, int K, int box_rows) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {kGroup, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    static const int n = [] {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        return sms;
+    }();
+    return n;
+}
+
+template <bool UP>
+int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaStream_t s) {
+    const int blocks = pr.N / kGroup, n_tiles = UP ? blocks : (blocks + 1) / 2;
+    // The most row tiles any windows over these rows can have.
+    const long long m_most = (long long)(pr.rows + kTileM - 1) / kTileM + min(pr.P, pr.rows);
+    if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
+    CUtensorMap map_a, map_w;
+    if (!byte_map(&map_a, a, (size_t)pr.rows, pr.K, kRowBox) ||
+        !byte_map(&map_w, w, (size_t)pr.P * (UP ? 2 : 1) * pr.N, pr.K, kGroup))
+        return MOE_ERR_CUDA;
+    const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(Barriers) + (size_t)(pr.P + 1) * sizeof(int);
+    if (cudaFuncSetAttribute(experts_kernel<UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int sms = sm_count();
+    if (sms < 1) return MOE_ERR_CUDA;
+    const unsigned grid = (unsigned)(m_most * n_tiles < sms ? m_most * n_tiles : sms);
+    return launch_pdl(experts_kernel<UP>, dim3(grid), dim3(kExpertsThreads), smem, s, map_a, map_w, pr) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -129,11 +505,9 @@ extern "C" MOE_API int moe_experts_up(const moe_experts* e, const uint8_t* codes
         if (!aligned16(p)) return MOE_ERR_ALIGN;
     }
     if (rows == 0) return MOE_OK;
-    cudaError_t c = launch_pdl(experts_kernel<true>, dim3(e->I / kGroup, e->P), dim3(kGroup), 0,
-                               static_cast<cudaStream_t>(stream), e->P, e->I, e->H, codes, scales, scale_stride,
-                               e->w13, e->s13, offsets, rows, h, h_scales, h_stride, (uint16_t*)nullptr,
-                               e->error_word);
-    return c == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const Problem pr = {e->P, e->I,     e->H, scales,   scale_stride, e->s13,  offsets,
+                        rows, h,        h_scales, h_stride, nullptr,      e->error_word};
+    return launch_experts<true>(pr, codes, e->w13, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" MOE_API int moe_experts_down(const moe_experts* e, const uint8_t* h, const float* h_scales,
@@ -149,8 +523,7 @@ extern "C" MOE_API int moe_experts_down(const moe_experts* e, const uint8_t* h, 
         if (!aligned16(p)) return MOE_ERR_ALIGN;
     }
     if (rows == 0) return MOE_OK;
-    cudaError_t c = launch_pdl(experts_kernel<false>, dim3(e->H / kGroup, e->P), dim3(kGroup), 0,
-                               static_cast<cudaStream_t>(stream), e->P, e->H, e->I, h, h_scales, h_stride, e->w2,
-                               e->s2, offsets, rows, (uint8_t*)nullptr, (float*)nullptr, 0, out, e->error_word);
-    return c == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const Problem pr = {e->P, e->H,    e->I,    h_scales, h_stride, e->s2,  offsets,
+                        rows, nullptr, nullptr, 0,        out,      e->error_word};
+    return launch_experts<false>(pr, h, e->w2, static_cast<cudaStream_t>(stream));
 }

@@ -354,8 +354,9 @@ typedef struct moe_experts {
  * Products of codes are summed in fp32 over each 128-element block on the
  * tensor cores, scaled by row scale x weight scale, and added up in fp32.
  * scale_stride, h_stride: multiples of 4 holding H / 128 and I / 128 groups.
- * A window outside the rows is skipped and sets MOE_DEVERR_WINDOW; rows of no
- * window are left as they are.  rows = 0: no-op.
+ * A window that leaves the rows, runs backwards or starts before an earlier
+ * offset is skipped and sets MOE_DEVERR_WINDOW; rows of no window are left as
+ * they are.  rows = 0: no-op.
  */
 MOE_API int moe_experts_up(const moe_experts* experts, const uint8_t* codes, const float* scales,
                            int32_t scale_stride, const int32_t* offsets, int32_t rows, uint8_t* h, float* h_scales,
