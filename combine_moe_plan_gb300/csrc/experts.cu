@@ -18,27 +18,39 @@ namespace {
 
 constexpr int kTileM = 128;        // rows of a tile (TMEM lanes)
 constexpr int kTileN = 256;        // outputs of a tile: two 128-blocks of weight rows
-constexpr int kStages = 4;         // operand buffers
 constexpr int kRowBox = 32;        // rows per TMA box of the row operand
 constexpr int kABytes = kTileM * kGroup;
 constexpr int kBHalf = kGroup * kGroup;
 constexpr int kStageBytes = kABytes + 2 * kBHalf;
 constexpr int kSumWarps = 8;       // warps that scale and add up
-constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
+constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kStoreWarp = kSumWarps + 2;
 constexpr int kExpertsThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
-// 256 x 224 + 128 x 48 = 63,488.
-constexpr int kSumRegs = 224, kOtherRegs = 48;
+// 256 x 232 + 128 x 40 = 64,512.
+constexpr int kSumRegs = 232, kOtherRegs = 40;
 constexpr int kHalfN = 64;         // columns of each 128-block that a summing warp owns
 
+// Finished rows wait in shared memory for the warp that copies them out, so
+// that the summing warps can begin the next tile.  Rows are padded by 16 bytes
+// (no bank conflicts); the pad holds the row's maxima (Up).  The bf16 tile
+// takes the room of one operand buffer: three are enough, for the loads in
+// flight at any time (21 MB over 152 SMs) are several times latency x bandwidth.
+template <bool UP>
+struct Layout {
+    static constexpr int kStages = UP ? 4 : 3;  // operand buffers
+    static constexpr int kPitch = (UP ? kGroup : 2 * kTileN) + 16;
+    static constexpr int kStagedBytes = kTileM * kPitch;
+    static constexpr int kBytes = kStages * kStageBytes + kStagedBytes;
+};
+
 struct Barriers {
-    uint64_t full[kStages], empty[kStages];  // operand buffers
-    uint64_t acc_full[2], acc_empty[2];      // TMEM accumulators of one 128-block of K
+    uint64_t full[4], empty[4];          // operand buffers
+    uint64_t acc_full[2], acc_empty[2];  // TMEM accumulators of one 128-block of K
+    uint64_t staged, stage_free;         // finished rows
     uint64_t drain;
     uint32_t tmem;
     int gave_up;
     int warp_total[kExpertsThreads / 32], warp_top[kExpertsThreads / 32];
-    float amax[2][2][kTileM];  // [tile parity][column half][row]
 };
 
 struct Problem {
@@ -146,17 +158,13 @@ __device__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, in
     return total;
 }
 
-// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e) held as a sum of
-// two floats, so that its relative error stays at the approximations' own
-// (2^-22 each) for every g; where exp overflows the quotient is 0.
+// g / (1 + exp(-g)) * u.  exp by 2^t with t = -g log2(e): the rounding of t
+// makes its relative error |g| 2^-24, next to 2^-22 for the approximations;
+// where |g| is large either exp(-g) or the whole product is negligible.  An
+// overflow gives the limit 0.
 __device__ __forceinline__ float gated(float g, float u) {
-    const float x = fminf(fmaxf(g, -200.0f), 100.0f);  // past these the limits are reached
-    const float t = x * -1.44269504f;
-    const float lo = fmaf(x, -1.44269504f, -t) - x * 1.925963033e-8f;
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = fminf(fmaf(e, lo * 0.693147181f, e), 3e38f);  // never NaN (fminf)
-    float r;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return g * r * u;
 }
@@ -164,9 +172,16 @@ __device__ __forceinline__ float gated(float g, float u) {
 template <bool UP>
 __global__ void __launch_bounds__(kExpertsThreads, 1)
 experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Problem pr) {
+    constexpr int kStages = Layout<UP>::kStages, kPitch = Layout<UP>::kPitch;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char* stages = smem + (1024u - (smem_u32(smem) & 1023u)) % 1024u;
-    Barriers& b = *reinterpret_cast<Barriers*>(stages + kStages * kStageBytes);
+    const uint32_t skip = (1024u - (smem_u32(smem) & 1023u)) % 1024u;  // 0 unless the base moved
+    unsigned char* stages = smem + skip;
+    unsigned char* staged = stages + kStages * kStageBytes;
+    Barriers& b = *reinterpret_cast<Barriers*>(stages + Layout<UP>::kBytes);
+    if (skip + Layout<UP>::kBytes + sizeof(Barriers) + (pr.P + 1) * sizeof(int) > dynamic_smem_bytes()) {
+        if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
+        return;
+    }
     int* first_m = reinterpret_cast<int*>(&b + 1);  // [P + 1]
     volatile int* gave_up = &b.gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,6 +196,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 mbar_init(&b.acc_full[s], 1);
                 mbar_init(&b.acc_empty[s], kSumWarps);
             }
+            mbar_init(&b.staged, kSumWarps);
+            mbar_init(&b.stage_free, 2);
             mbar_init(&b.drain, 1);
             b.gave_up = 0;
             mbar_init_fence();
@@ -245,22 +262,28 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             int s = 0;
             uint32_t phase = 0, it = 0;
             bool ok = true;
+            const uint64_t desc_a = umma_desc(stages), desc_w = umma_desc(stages + kABytes);
             for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
                 const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
                 const bool two = UP || 2 * t.n + 1 < blocks;
                 const uint32_t idesc = umma_idesc_e4m3(kTileM, two ? kTileN : kGroup);
                 for (int k = 0; k < kb; ++k, ++it) {
                     const uint32_t buf = it & 1;
-                    if (!(ok = mbar_wait(&b.acc_empty[buf], ((it >> 1) & 1) ^ 1, gave_up))) break;
                     if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
+                    if (!(ok = mbar_wait(&b.acc_empty[buf], ((it >> 1) & 1) ^ 1, gave_up))) break;
                     tc_fence_after();
-                    const uint64_t da = umma_desc(stages + s * kStageBytes);
-                    const uint64_t dw = umma_desc(stages + s * kStageBytes + kABytes);
+                    const uint64_t da = desc_a + (uint32_t)s * (kStageBytes / 16);
+                    const uint64_t dw = desc_w + (uint32_t)s * (kStageBytes / 16);
+                    const uint32_t d = tmem + buf * kTileN;
 #pragma unroll
-                    for (int i = 0; i < kGroup / 32; ++i)
-                        umma_e4m3(tmem + buf * kTileN, da + 2 * i, dw + 2 * i, idesc, i != 0);
-                    umma_commit(&b.empty[s]);
+                    for (int i = 0; i < kGroup / 32; ++i) {
+                        if (i == 0)
+                            umma_e4m3<false>(d, da, dw, idesc);
+                        else
+                            umma_e4m3<true>(d, da + 2 * i, dw + 2 * i, idesc);
+                    }
                     umma_commit(&b.acc_full[buf]);
+                    umma_commit(&b.empty[s]);
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1;
@@ -275,45 +298,80 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 }
             }
         }
+        if (warp >= kStoreWarp) {
+            // Copy finished rows out, 16 bytes a lane: 512-byte rows of bf16 by
+            // the whole warp (a single block: half of it idles), 128-byte rows
+            // of codes four at a time.  The two warps take alternate groups.
+            constexpr int kLanes = (UP ? kGroup : 2 * kTileN) / 16, kRows = 32 / kLanes, kBatch = UP ? 4 : 2;
+            const int sub = lane / kLanes, col = (lane % kLanes) * 16;
+            uint32_t parity = 0;
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, parity ^= 1) {
+                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                const bool mine = UP || 2 * t.n + 1 < blocks || col < 2 * kGroup;
+                unsigned char* dst = UP ? pr.h + (size_t)t.n * kGroup + col
+                                        : reinterpret_cast<unsigned char*>(pr.out + (size_t)t.n * kTileN) + col;
+                const size_t pitch = UP ? (size_t)pr.N : 2 * (size_t)pr.N;
+                if (!mbar_wait_warp(&b.staged, parity, gave_up)) break;
+                for (int r0 = (warp - kStoreWarp) * kBatch * kRows; r0 < t.valid; r0 += 2 * kBatch * kRows) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        v[i] = *reinterpret_cast<const uint4*>(staged + (r0 + i * kRows + sub) * kPitch + col);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i * kRows + sub;
+                        if (mine && r < t.valid) st16(dst + (size_t)(t.row + r) * pitch, v[i]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.stage_free);
+            }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // Summing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
         // thread) and of each 128-block the columns 64 (w / 4) .. + 63.
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalfN;
+        const int in_tile = quarter * 32 + lane;
         uint32_t it = 0, parity = 0;
         bool ok = true;
-        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, parity ^= 1) {
-            const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
-            const bool two = UP || 2 * t.n + 1 < blocks;
-            const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
-            const int in_tile = quarter * 32 + lane;
-            const size_t row = (size_t)t.row + min(in_tile, t.valid - 1);
-            const float* sa = pr.sa + row * pr.sa_stride;
+        // Each tile is looked up, and its first scales are loaded, while the
+        // one before it is summed.
+        Tile t = {0, 0, 0, 0}, next = t;
+        const float *sa = nullptr, *sw = nullptr;  // scales of the row and of the first 128-block
+        int gap = 0;                               // from there to the second block's
+        float ar = 0.0f, f0 = 0.0f, f1 = 0.0f;
+        const auto begin = [&](const Tile& n) {
+            t = n;
+            sa = pr.sa + ((size_t)t.row + min(in_tile, t.valid - 1)) * pr.sa_stride;
             const int blk = UP ? t.n : 2 * t.n;
-            const float* sw0 = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
-            const float* sw1 = UP ? sw0 + (size_t)blocks * kb : (two ? sw0 + kb : sw0);
+            sw = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
+            gap = UP ? blocks * kb : (blk + 1 < blocks ? kb : 0);
+            ar = __ldg(sa);
+            f0 = __ldg(sw);
+            f1 = __ldg(sw + gap);
+        };
+        if (blockIdx.x < tiles) begin(walk.at((int)blockIdx.x, n_tiles, first_m, pr.offsets, pr.P));
+        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, parity ^= 1) {
+            const bool more = tile + gridDim.x < tiles;
+            const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
+            const Tile now = t;
             uint64_t acc[2][kHalfN / 2];
 #pragma unroll
             for (int i = 0; i < kHalfN / 2; ++i) acc[0][i] = acc[1][i] = 0ull;
-            float4 a4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (busy) a4 = __ldg(reinterpret_cast<const float4*>(sa));
-            float4 next = a4;
-            float f0 = __ldg(sw0), f1 = __ldg(sw1);
             for (int k = 0; k < kb; ++k, ++it) {
                 const uint32_t buf = it & 1;
-                if ((k & 3) == 0) {
-                    a4 = next;
-                    if (busy && k + 4 < kb) next = __ldg(reinterpret_cast<const float4*>(sa + k + 4));
-                }
-                const float ar = (k & 2) ? ((k & 1) ? a4.w : a4.z) : ((k & 1) ? a4.y : a4.x);
                 const float s0 = ar * f0, s1 = ar * f1;
-                if (k + 1 < kb) {
-                    f0 = __ldg(sw0 + k + 1);
-                    f1 = __ldg(sw1 + k + 1);
+                if (k == 0 && more) next = walk.at((int)(tile + gridDim.x), n_tiles, first_m, pr.offsets, pr.P);
+                if (k + 1 < kb) {  // the next block's scales, a block ahead
+                    ar = __ldg(sa + k + 1);
+                    f0 = __ldg(sw + k + 1);
+                    f1 = __ldg(sw + gap + k + 1);
+                } else if (more) {
+                    begin(next);
                 }
-                if (!(ok = mbar_wait(&b.acc_full[buf], (it >> 1) & 1, gave_up))) break;
-                __syncwarp();
+                if (!(ok = mbar_wait_warp(&b.acc_full[buf], (it >> 1) & 1, gave_up))) break;
                 tc_fence_after();
                 if (busy) {
                     const uint64_t s2[2] = {pack2(__float_as_uint(s0), __float_as_uint(s0)),
@@ -342,7 +400,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (UP) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");  // let the partner go on
                 break;
             }
-            const bool store = in_tile < t.valid;
+            unsigned char* mine = staged + in_tile * kPitch;
             if constexpr (UP) {
                 float amax = 0.0f;
                 if (busy) {
@@ -355,43 +413,50 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
                 // the row's other 64 columns are with the warp 4 further (or back)
-                b.amax[parity][half][in_tile] = amax;
+                float* maxima = reinterpret_cast<float*>(mine + kGroup) + 2 * parity;
+                maxima[half] = amax;
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                amax = fmaxf(amax, b.amax[parity][half ^ 1][in_tile]);
-                if (store) {
+                amax = fmaxf(amax, maxima[half ^ 1]);
+                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) break;
+                if (busy) {
                     // a tiny group is scaled up first, so that 448 / amax stays finite
                     const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
                     const float inv = amax > 0.0f ? kE4M3Max / (amax * lift) : 0.0f;
-                    uint32_t q[kHalfN / 4];
 #pragma unroll
-                    for (int i = 0; i < kHalfN / 4; ++i) {
-                        const float2 x = unpack2(acc[0][2 * i]), y = unpack2(acc[0][2 * i + 1]);
-                        q[i] = pack_e4m3x2(x.x * lift * inv, x.y * lift * inv) |
-                               pack_e4m3x2(y.x * lift * inv, y.y * lift * inv) << 16;
-                    }
-                    uint8_t* dst = pr.h + row * pr.N + (size_t)t.n * kGroup + half * kHalfN;
-#pragma unroll
-                    for (int i = 0; i < kHalfN / 16; ++i)
-                        st16(dst + 16 * i, make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]));
-                    if (half == 0) pr.hs[row * pr.hs_stride + t.n] = amax / kE4M3Max;
-                }
-            } else if (store) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c == 1 && !two) break;
-                    uint16_t* dst = pr.out + row * pr.N + (size_t)(2 * t.n + c) * kGroup + half * kHalfN;
-#pragma unroll
-                    for (int i = 0; i < kHalfN / 8; ++i) {
+                    for (int i = 0; i < kHalfN / 16; ++i) {
                         uint32_t q[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float2 x = unpack2(acc[c][4 * i + j]);
-                            q[j] = pack_bf16x2_rn(x.x, x.y);
+                            const float2 x = unpack2(acc[0][8 * i + 2 * j]), y = unpack2(acc[0][8 * i + 2 * j + 1]);
+                            q[j] = pack_e4m3x2(x.x * lift * inv, x.y * lift * inv) |
+                                   pack_e4m3x2(y.x * lift * inv, y.y * lift * inv) << 16;
                         }
-                        st16(dst + 8 * i, make_uint4(q[0], q[1], q[2], q[3]));
+                        st_shared16(mine + half * kHalfN + 16 * i, make_uint4(q[0], q[1], q[2], q[3]));
+                    }
+                    if (half == 0 && in_tile < now.valid)
+                        pr.hs[((size_t)now.row + in_tile) * pr.hs_stride + now.n] = amax / kE4M3Max;
+                }
+            } else {
+                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) break;
+                if (busy) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < kHalfN / 8; ++i) {
+                            uint32_t q[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 x = unpack2(acc[c][4 * i + j]);
+                                q[j] = pack_bf16x2_rn(x.x, x.y);
+                            }
+                            st_shared16(mine + 2 * (c * kGroup + half * kHalfN + 8 * i),
+                                        make_uint4(q[0], q[1], q[2], q[3]));
+                        }
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.staged);
         }
         if (!ok && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
         tc_fence_before();
@@ -462,7 +527,7 @@ int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaSt
     if (!byte_map(&map_a, a, (size_t)pr.rows, pr.K, kRowBox) ||
         !byte_map(&map_w, w, (size_t)pr.P * (UP ? 2 : 1) * pr.N, pr.K, kGroup))
         return MOE_ERR_CUDA;
-    const size_t smem = 1024 + (size_t)kStages * kStageBytes + sizeof(Barriers) + (size_t)(pr.P + 1) * sizeof(int);
+    const size_t smem = Layout<UP>::kBytes + sizeof(Barriers) + (size_t)(pr.P + 1) * sizeof(int);
     if (cudaFuncSetAttribute(experts_kernel<UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
         return MOE_ERR_CUDA;

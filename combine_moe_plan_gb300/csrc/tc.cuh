@@ -12,6 +12,19 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One lane of a converged warp, the same one every time.  (The compiler knows
+// that code under this predicate runs in one lane and keeps descriptors in
+// uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
 // ---- mbarriers (shared memory, 8 bytes each) ----
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -23,21 +36,24 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+constexpr uint32_t kPollNs = 1000000;  // a poll may sleep this long; it wakes when the phase ends
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
         : "memory");
     return ok != 0;
 }
 
-// Waits are bounded: after kStallNs (and at least kStallTries polls, so that a
-// preempted CTA is not blamed) the wait gives up, tells the CTA's other waits
-// through *gave_up, and returns false.
+// Waits are bounded: a wait that is not over after kStallTries polls (tens of
+// microseconds) starts a clock, and gives up kStallNs later; it then tells the
+// CTA's other waits through *gave_up and returns false.  The clock is not read
+// before that: reading %globaltimer takes several hundred cycles, which every
+// wait that is not over at its first poll would pay.
 constexpr uint64_t kStallNs = 4000000000ull;
 constexpr int kStallTries = 4096;
 
@@ -47,20 +63,21 @@ __device__ __forceinline__ uint64_t now_ns() {
     return t;
 }
 
-static __device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    const uint64_t t0 = now_ns();
-    for (int i = 0;; i = i < kStallTries ? i + 1 : i) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    for (int i = 0; i < kStallTries; ++i)
+        if (mbar_try(bar, parity)) return true;
+    for (const uint64_t t0 = now_ns();;) {
         if (mbar_try(bar, parity)) return true;
         if (*gave_up) return false;
-        if (i >= kStallTries && now_ns() - t0 > kStallNs) {
+        if (now_ns() - t0 > kStallNs) {
             *gave_up = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, gave_up);
+// The same for a converged warp, which stays converged.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, gave_up));
 }
 
 // ---- TMA: one box of a two-dimensional tensor into shared memory; (x, y) is
@@ -73,6 +90,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
+}
+
+// ---- shared memory ----
+__device__ __forceinline__ void st_shared16(void* p, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(p)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t dynamic_smem_bytes() {
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
 }
 
 // ---- TMEM ----
@@ -121,12 +149,13 @@ __device__ __forceinline__ uint64_t umma_desc(const void* smem) {
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(m / 16) << 24);
 }
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <bool ACCUMULATE>
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
         : "memory");
 }
 // Arrive on `bar` when every tcgen05 operation this thread issued is done.

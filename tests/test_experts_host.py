@@ -125,11 +125,16 @@ def test_binding_checks_tensors():
     """The binding refuses tensors that the call would misread."""
     f8 = torch.float8_e4m3fn
     ok = torch.zeros(4, 8, dtype=f8)
-    moe._tensor("x", ok, f8, (4, 8))
-    moe._tensor("x", ok, f8, (None, 8), 3)
+    moe._tensor("x", ok, f8, 4, 8)
+    moe._tensor("x", ok, f8, 3)
     for bad in (ok.view(torch.int8), ok.t(), ok[:, :4], ok[:2], ok.view(-1)):
         with pytest.raises(ValueError):
-            moe._tensor("x", bad, f8, (None, 8), 4)
+            moe._tensor("x", bad, f8, 4, 8)
+    w, s = torch.zeros(2, 256, 128, dtype=f8), torch.zeros(2, 2, 1)
+    moe._block_scaled("w2", w, s, 2, 256, 128)
+    for bad_w, bad_s in ((w.view(torch.int8), s), (w[:1], s), (w, s[:1]), (w, s.double()), (w.transpose(1, 2), s)):
+        with pytest.raises(ValueError):
+            moe._block_scaled("w2", bad_w, bad_s, 2, 256, 128)
     with pytest.raises(ValueError):
         moe.Experts()
     with pytest.raises(ValueError):
