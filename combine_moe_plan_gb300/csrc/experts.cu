@@ -23,12 +23,13 @@ constexpr int kABytes = kTileM * kGroup;
 constexpr int kBHalf = kGroup * kGroup;
 constexpr int kStageBytes = kABytes + 2 * kBHalf;
 constexpr int kSumWarps = 8;       // warps that scale and add up
+constexpr int kColGroups = kSumWarps / 4;  // warps that share a row
 constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kStoreWarp = kSumWarps + 2;
 constexpr int kExpertsThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
 // 256 x 232 + 128 x 40 = 64,512.
 constexpr int kSumRegs = 232, kOtherRegs = 40;
-constexpr int kHalfN = 64;         // columns of each 128-block that a summing warp owns
+constexpr int kHalfN = kGroup / kColGroups;  // columns of each 128-block that a summing warp owns
 
 // Finished rows wait in shared memory for the warp that copies them out, so
 // that the summing warps can begin the next tile.  Rows are padded by 16 bytes
@@ -184,7 +185,9 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     int* first_m = reinterpret_cast<int*>(&b + 1);  // [P + 1]
     volatile int* gave_up = &b.gave_up;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Uniform in a warp, and through the shuffle known to be: with elect_one it
+    // lets the roles of one thread keep their addresses in uniform registers.
+    const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
@@ -224,7 +227,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
     if (warp >= kSumWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kTmaWarp && lane == 0) {
+        if (warp == kTmaWarp && elect_one()) {
             int s = 0;
             uint32_t phase = 0, issued = 0;
             bool ok = true;
@@ -258,7 +261,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
             }
         }
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp && elect_one()) {
             int s = 0;
             uint32_t phase = 0, it = 0;
             bool ok = true;
@@ -397,7 +400,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (lane == 0) mbar_arrive(&b.acc_empty[buf]);
             }
             if (!ok) {
-                if (UP) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");  // let the partner go on
+                if (UP) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");  // let the partner go on
                 break;
             }
             unsigned char* mine = staged + in_tile * kPitch;
@@ -413,11 +416,14 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
                 // the row's other 64 columns are with the warp 4 further (or back)
-                float* maxima = reinterpret_cast<float*>(mine + kGroup) + 2 * parity;
+                float* maxima = reinterpret_cast<float*>(mine + kGroup);
+                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) {
+                    asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");
+                    break;
+                }
                 maxima[half] = amax;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                amax = fmaxf(amax, maxima[half ^ 1]);
-                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) break;
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");
+                for (int i = 0; i < kColGroups; ++i) amax = fmaxf(amax, maxima[i]);
                 if (busy) {
                     // a tiny group is scaled up first, so that 448 / amax stays finite
                     const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
