@@ -31,6 +31,12 @@ constexpr int kExpertsThreads = 32 * (kSumWarps + 4);  // three warpgroups
 constexpr int kSumRegs = 232, kOtherRegs = 40;
 constexpr int kHalfN = kGroup / kColGroups;  // columns of each 128-block that a summing warp owns
 
+// The loading thread looks each tile up and leaves it in a ring for the other
+// warps (a lookup costs about 1.5 k cycles of latency, which the summing warps
+// cannot hide).  It runs ahead of the last reader by at most the operand
+// buffers, the accumulators and a staged tile: 4 + 2 + 2 tiles of one block.
+constexpr int kTileRing = 16;
+
 // Finished rows wait in shared memory for the warp that copies them out, so
 // that the summing warps can begin the next tile.  Rows are padded by 16 bytes
 // (no bank conflicts); the pad holds the row's maxima (Up).  The bf16 tile
@@ -44,11 +50,13 @@ struct Layout {
     static constexpr int kBytes = kStages * kStageBytes + kStagedBytes;
 };
 
-struct Barriers {
+struct alignas(16) Barriers {
     uint64_t full[4], empty[4];          // operand buffers
     uint64_t acc_full[2], acc_empty[2];  // TMEM accumulators of one 128-block of K
     uint64_t staged, stage_free;         // finished rows
+    uint64_t known[kTileRing];           // tiles[i] is written
     uint64_t drain;
+    int4 tiles[kTileRing];  // expert, n, row, valid
     uint32_t tmem;
     int gave_up;
     int warp_total[kExpertsThreads / 32], warp_top[kExpertsThreads / 32];
@@ -77,13 +85,24 @@ struct Tile {
 
 // Tiles in the order (expert, n, rows), rows fastest: CTAs working side by
 // side share a block of weights.  first_m[p] counts the row tiles before
-// expert p.  Tile indices only grow, so the expert is found by moving on.
+// expert p; the expert is found by bisection from the last one on (tile indices
+// only grow), not step by step: a few rows over hundreds of experts leave most
+// of them empty (walking past them took 2 us of a single token's 46).
 struct TileWalk {
     int p = 0;
     __device__ __forceinline__ Tile at(int tile, int n_tiles, const int* first_m, const int32_t* offsets,
                                        int P) {
         const int m_index = tile / n_tiles;
-        while (p + 1 < P && first_m[p + 1] <= m_index) ++p;
+        if (first_m[p + 1] <= m_index) {
+            int past = P;
+            while (past - p > 1) {
+                const int mid = (p + past) >> 1;
+                if (first_m[mid] <= m_index)
+                    p = mid;
+                else
+                    past = mid;
+            }
+        }
         const int m_tiles = first_m[p + 1] - first_m[p];
         const int local = tile - first_m[p] * n_tiles;
         Tile t;
@@ -96,34 +115,30 @@ struct TileWalk {
     }
 };
 
-// The largest value of the threads before this one (0 for the first).
-__device__ __forceinline__ int block_max_before(int v, int* warp_top) {
+// First row tile of every expert, in shared memory; returns their number.  A
+// window that leaves the rows, runs backwards or starts before an earlier
+// offset (it could share rows with an earlier window) counts as empty and is
+// reported.  Whole CTA.
+__device__ __forceinline__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, int* warp_top) {
+    constexpr int kWarps = kExpertsThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = v;
+    const int per = (pr.P + kExpertsThreads - 1) / kExpertsThreads;
+    const int lo = min(pr.P, (int)threadIdx.x * per), hi = min(pr.P, lo + per);
+    // the largest offset before this thread's first
+    int top = 0;
+    for (int p = lo; p < hi; ++p) top = max(top, pr.offsets[p]);
+    int incl = top;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(kFull, incl, off);
         if (lane >= off) incl = max(incl, o);
     }
     if (lane == 31) warp_top[warp] = incl;
-    int before = __shfl_up_sync(kFull, incl, 1);
-    if (lane == 0) before = 0;
+    top = __shfl_up_sync(kFull, incl, 1);
+    if (lane == 0) top = 0;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before = max(before, warp_top[w]);
-    return before;
-}
+    top = max(top, __reduce_max_sync(kFull, lane < warp ? warp_top[lane] : 0));
 
-// First row tile of every expert, in shared memory; returns their number.  A
-// window that leaves the rows, runs backwards or starts before an earlier
-// offset (it could share rows with an earlier window) counts as empty and is
-// reported.
-__device__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, int* warp_top) {
-    const int per = (pr.P + kExpertsThreads - 1) / kExpertsThreads;
-    const int lo = min(pr.P, (int)threadIdx.x * per), hi = min(pr.P, lo + per);
-    // the largest offset before this thread's first
-    int top = 0;
-    for (int p = lo; p < hi; ++p) top = max(top, pr.offsets[p]);
-    top = block_max_before(top, warp_top);
     int sum = 0;
     for (int p = lo; p < hi; ++p) {
         const int a = pr.offsets[p], b = pr.offsets[p + 1];
@@ -134,8 +149,7 @@ __device__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, in
         first_m[p] = m;
         sum += m;
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = sum;
+    incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(kFull, incl, off);
@@ -143,12 +157,9 @@ __device__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, in
     }
     if (lane == 31) warp_total[warp] = incl;
     __syncthreads();
-    int base = 0, total = 0;
-    for (int w = 0; w < kExpertsThreads / 32; ++w) {
-        if (w < warp) base += warp_total[w];
-        total += warp_total[w];
-    }
-    int run = base + incl - sum;
+    const int mine = lane < kWarps ? warp_total[lane] : 0;
+    const int total = __reduce_add_sync(kFull, mine);
+    int run = __reduce_add_sync(kFull, lane < warp ? mine : 0) + incl - sum;
     for (int p = lo; p < hi; ++p) {
         const int m = first_m[p];
         first_m[p] = run;
@@ -201,6 +212,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
             mbar_init(&b.staged, kSumWarps);
             mbar_init(&b.stage_free, 2);
+            for (int i = 0; i < kTileRing; ++i) mbar_init(&b.known[i], 1);
             mbar_init(&b.drain, 1);
             b.gave_up = 0;
             mbar_init_fence();
@@ -223,29 +235,49 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int width = UP ? 2 * pr.N : pr.N;                 // weight rows per expert
     const int kb = pr.K / kGroup;
     const long long tiles = (long long)m_total * n_tiles;   // at most 2^31: checked by the host
-    TileWalk walk;
+    // Tile number j of this CTA, once the loading thread has left it in the ring.
+    const auto known_tile = [&](uint32_t j, Tile* t) {
+        const int i = j % kTileRing;
+        if (!mbar_wait(&b.known[i], (j / kTileRing) & 1, gave_up)) return false;
+        const int4 v = *const_cast<const int4*>(&b.tiles[i]);
+        *t = {v.x, v.y, v.z, v.w};
+        return true;
+    };
 
     if (warp >= kSumWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kTmaWarp && elect_one()) {
             int s = 0;
             uint32_t phase = 0, issued = 0;
+            uint32_t used = 0x04040404u * (kTileM / kRowBox / 4);  // boxes holding something, 8 bits a buffer
             bool ok = true;
-            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            TileWalk walk;
+            uint32_t j = 0;
+            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
                 const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                b.tiles[j % kTileRing] = make_int4(t.p, t.n, t.row, t.valid);
+                mbar_arrive(&b.known[j % kTileRing]);
                 const int w0 = t.p * width + (UP ? t.n : 2 * t.n) * kGroup;
                 const bool two = UP || 2 * t.n + 1 < blocks;
                 const int w1 = UP ? w0 + pr.N : w0 + kGroup;
-                const int boxes = (t.valid + kRowBox - 1) / kRowBox;
-                const uint32_t bytes = boxes * kRowBox * kGroup + (two ? 2 : 1) * kBHalf;
+                const uint32_t boxes = (t.valid + kRowBox - 1) / kRowBox;
+                const uint32_t weight_bytes = (two ? 2 : 1) * kBHalf;
                 for (int k = 0; k < kb; ++k) {
                     if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
                     unsigned char* a = stages + s * kStageBytes;
-                    mbar_expect_tx(&b.full[s], bytes);
+                    // Rows of an earlier, fuller tile are cleared (by boxes past
+                    // the end of the rows, which read nothing): their products
+                    // would be thrown away, but not for free on a GPU that runs
+                    // at its power limit.
+                    const uint32_t held = (used >> (8 * s)) & 0xffu;
+                    const uint32_t top = max(boxes, held);
+                    used = (used & ~(0xffu << (8 * s))) | boxes << (8 * s);
+                    mbar_expect_tx(&b.full[s], top * kRowBox * kGroup + weight_bytes);
                     tma_load_2d(a + kABytes, &map_w, k * kGroup, w0, &b.full[s]);
                     if (two) tma_load_2d(a + kABytes + kBHalf, &map_w, k * kGroup, w1, &b.full[s]);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(a + i * kRowBox * kGroup, &map_a, k * kGroup, t.row + i * kRowBox, &b.full[s]);
+                    for (uint32_t i = 0; i < top; ++i)
+                        tma_load_2d(a + i * kRowBox * kGroup, &map_a, k * kGroup,
+                                    i < boxes ? t.row + (int)(i * kRowBox) : pr.rows, &b.full[s]);
                     ++issued;
                     if (++s == kStages) {
                         s = 0;
@@ -266,8 +298,10 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             uint32_t phase = 0, it = 0;
             bool ok = true;
             const uint64_t desc_a = umma_desc(stages), desc_w = umma_desc(stages + kABytes);
-            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+            uint32_t j = 0;
+            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
+                Tile t;
+                if (!UP && !(ok = known_tile(j, &t))) break;
                 const bool two = UP || 2 * t.n + 1 < blocks;
                 const uint32_t idesc = umma_idesc_e4m3(kTileM, two ? kTileN : kGroup);
                 for (int k = 0; k < kb; ++k, ++it) {
@@ -307,14 +341,15 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             // of codes four at a time.  The two warps take alternate groups.
             constexpr int kLanes = (UP ? kGroup : 2 * kTileN) / 16, kRows = 32 / kLanes, kBatch = UP ? 4 : 2;
             const int sub = lane / kLanes, col = (lane % kLanes) * 16;
-            uint32_t parity = 0;
-            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, parity ^= 1) {
-                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+            uint32_t j = 0;
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+                Tile t;
+                if (!__all_sync(kFull, known_tile(j, &t))) break;
                 const bool mine = UP || 2 * t.n + 1 < blocks || col < 2 * kGroup;
                 unsigned char* dst = UP ? pr.h + (size_t)t.n * kGroup + col
                                         : reinterpret_cast<unsigned char*>(pr.out + (size_t)t.n * kTileN) + col;
                 const size_t pitch = UP ? (size_t)pr.N : 2 * (size_t)pr.N;
-                if (!mbar_wait_warp(&b.staged, parity, gave_up)) break;
+                if (!mbar_wait_warp(&b.staged, j & 1, gave_up)) break;
                 for (int r0 = (warp - kStoreWarp) * kBatch * kRows; r0 < t.valid; r0 += 2 * kBatch * kRows) {
                     uint4 v[kBatch];
 #pragma unroll
@@ -337,16 +372,16 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalfN;
         const int in_tile = quarter * 32 + lane;
-        uint32_t it = 0, parity = 0;
+        uint32_t it = 0, j = 0;
         bool ok = true;
-        // Each tile is looked up, and its first scales are loaded, while the
-        // one before it is summed.
-        Tile t = {0, 0, 0, 0}, next = t;
+        Tile t = {0, 0, 0, 0};
         const float *sa = nullptr, *sw = nullptr;  // scales of the row and of the first 128-block
         int gap = 0;                               // from there to the second block's
         float ar = 0.0f, f0 = 0.0f, f1 = 0.0f;
-        const auto begin = [&](const Tile& n) {
-            t = n;
+        // Tile j and its first scales: loaded before the tile in front of it is
+        // finished and stored, and needed after.
+        const auto begin = [&]() {
+            if (!__all_sync(kFull, known_tile(j, &t))) return false;
             sa = pr.sa + ((size_t)t.row + min(in_tile, t.valid - 1)) * pr.sa_stride;
             const int blk = UP ? t.n : 2 * t.n;
             sw = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
@@ -354,25 +389,21 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             ar = __ldg(sa);
             f0 = __ldg(sw);
             f1 = __ldg(sw + gap);
+            return true;
         };
-        if (blockIdx.x < tiles) begin(walk.at((int)blockIdx.x, n_tiles, first_m, pr.offsets, pr.P));
-        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, parity ^= 1) {
-            const bool more = tile + gridDim.x < tiles;
+        if (blockIdx.x < tiles) ok = begin();
+        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
             const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
-            const Tile now = t;
             uint64_t acc[2][kHalfN / 2];
 #pragma unroll
             for (int i = 0; i < kHalfN / 2; ++i) acc[0][i] = acc[1][i] = 0ull;
             for (int k = 0; k < kb; ++k, ++it) {
                 const uint32_t buf = it & 1;
                 const float s0 = ar * f0, s1 = ar * f1;
-                if (k == 0 && more) next = walk.at((int)(tile + gridDim.x), n_tiles, first_m, pr.offsets, pr.P);
                 if (k + 1 < kb) {  // the next block's scales, a block ahead
                     ar = __ldg(sa + k + 1);
                     f0 = __ldg(sw + k + 1);
                     f1 = __ldg(sw + gap + k + 1);
-                } else if (more) {
-                    begin(next);
                 }
                 if (!(ok = mbar_wait_warp(&b.acc_full[buf], (it >> 1) & 1, gave_up))) break;
                 tc_fence_after();
@@ -403,6 +434,10 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (UP) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");  // let the partner go on
                 break;
             }
+            const Tile now = t;
+            const uint32_t parity = j & 1;
+            ++j;
+            if (tile + gridDim.x < tiles) ok = begin();  // a failure ends the loop after this tile
             unsigned char* mine = staged + in_tile * kPitch;
             if constexpr (UP) {
                 float amax = 0.0f;
