@@ -154,6 +154,8 @@ struct TopkSoftmax {
 // The softmax's sum is carried as a pair of floats, so it does not depend on
 // the order of its terms: the choices, and with them every integer the plan
 // writes, are functions of the inputs alone, whatever the lanes per token.
+// (64-bit fixed point would do as well; its conversions cost 0.4 us more a plan
+// of 96 tokens.)
 struct ScoreRouter {
     static constexpr bool kScored = true;
     const float* bias;  // [E] or NULL
@@ -237,6 +239,30 @@ __device__ __forceinline__ void keep_best_groups(const ScoreRouter& ro, int E, i
         if (e0 + r < E && !((kept >> ((e0 + r) / size)) & 1u)) key[r] = 0u;
 }
 
+// v[r] = src[e0 + r] for the r < st with e0 + r < n, else `other`.
+template <int N>
+__device__ __forceinline__ void load_run(const float* __restrict__ src, int n, int e0, int st, bool quads, float other,
+                                         float (&v)[N]) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) v[r] = other;
+    if (N >= 4 && quads) {
+#pragma unroll
+        for (int r = 0; r + 3 < N; r += 4) {
+            if (r < st && e0 + r < n) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(src + e0 + r));
+                v[r] = q.x;
+                v[r + 1] = q.y;
+                v[r + 2] = q.z;
+                v[r + 3] = q.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            if (r < st && e0 + r < n) v[r] = __ldg(src + e0 + r);
+    }
+}
+
 // The keys of a scored router: the order keys of the choices of experts
 // [e0, e0 + st) of one token (0 past E and for a token past T), groups
 // applied.  A segment of L lanes holds a token; every lane of the warp takes
@@ -246,26 +272,11 @@ __device__ __forceinline__ void scored_keys(const ScoreRouter& ro, const float* 
                                             int e0, int st, int sl, uint32_t (&key)[EPL], float2* stat) {
     float v[EPL];
     const bool quads = ((st | E) & 3) == 0;  // 16-byte aligned runs of four
-#pragma unroll
-    for (int r = 0; r < EPL; ++r) v[r] = -INFINITY;
-    if (tok_ok) {
-        if (EPL >= 4 && quads) {
-#pragma unroll
-            for (int r = 0; r + 3 < EPL; r += 4) {
-                if (r < st && e0 + r < E) {
-                    const float4 q = __ldg(reinterpret_cast<const float4*>(row + e0 + r));
-                    v[r] = q.x;
-                    v[r + 1] = q.y;
-                    v[r + 2] = q.z;
-                    v[r + 3] = q.w;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < EPL; ++r)
-                if (r < st && e0 + r < E) v[r] = __ldg(row + e0 + r);
-        }
-    }
+    load_run(row, tok_ok ? E : 0, e0, st, quads, -INFINITY, v);
+    // The biases travel with the logits where registers allow.
+    constexpr int kEarly = EPL <= 8 ? EPL : 1;
+    float early[kEarly];
+    if (EPL <= 8 && ro.bias != nullptr) load_run(ro.bias, E, e0, st, quads, 0.0f, early);
     float2 ms = make_float2(0.0f, 1.0f);
     if (!ro.sigmoid) {
         float m = v[0];
@@ -276,8 +287,8 @@ __device__ __forceinline__ void scored_keys(const ScoreRouter& ro, const float* 
         dword::dw sum = {0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < EPL; ++r) {
-            float e = (r < st && e0 + r < E) ? expf(v[r] - m) : 0.0f;
-            if (!(e == e)) e = 0.0f;  // a NaN logit, or no finite one
+            float e = expf(v[r] - m);  // 0 past E
+            if (!(e == e)) e = 0.0f;   // a NaN logit, or no finite one
             const dword::dw t = dword::two_sum(sum.h, e);
             sum = dword::fast_two_sum(t.h, sum.l + t.l);
         }
@@ -293,7 +304,7 @@ __device__ __forceinline__ void scored_keys(const ScoreRouter& ro, const float* 
         key[r] = 0u;
         if (tok_ok && r < st && e < E) {
             float c = ro.score(v[r], ms);
-            if (ro.bias != nullptr) c += __ldg(ro.bias + e);
+            if (ro.bias != nullptr) c += EPL <= 8 ? early[r < kEarly ? r : 0] : __ldg(ro.bias + e);
             key[r] = order_key(c == c ? c : -INFINITY);
         }
     }
@@ -394,11 +405,13 @@ __device__ __forceinline__ void route_tile(const R& router, const float* __restr
     // after which the winning lane marks the slot taken and promotes its
     // second key (rescanning only when it has none left).  Key 0 sits below
     // every finite logit and marks padding.  Lane j keeps the j-th winner and
-    // its key, whose inverse is the selected logit.  Every lane runs the
-    // rounds (a token past T has only padding keys and writes nothing), so
-    // the segment butterflies below always see a converged warp.
-    {
-        const bool tok_ok = t < T;
+    // its key, whose inverse is the selected logit.  Where a warp holds several
+    // tokens every lane runs the rounds (a token past T has only padding keys
+    // and writes nothing), so the segment butterflies below always see a
+    // converged warp; a whole warp past T skips them (its lanes would rescan
+    // their empty keys every round: 1.7 us of a one-token plan's 6).
+    const bool tok_ok = t < T;
+    if (L < 32 || tok_ok) {
         const float* row = logits + (size_t)(tok_ok ? t : t0) * E;
         uint32_t key[EPL];
         // expert of slot r: first + r * step
@@ -423,7 +436,14 @@ __device__ __forceinline__ void route_tile(const R& router, const float* __restr
         for (int j = 0; j < k; ++j) {
             uint32_t m;
             int win;
-            if (L == 32) {  // whole warp: redux.sync (26 cycles on GB300)
+            if (L == 32 && R::kScored) {
+                // Lanes hold ascending runs of experts, so of equal keys the
+                // lowest lane's is the lowest expert: a ballot finds it (a third
+                // less latency a round than a second redux.sync on the ids).
+                m = __reduce_max_sync(kFull, k1);
+                const int lane_w = __ffs(__ballot_sync(kFull, k1 == m)) - 1;
+                win = (int)__shfl_sync(kFull, cand, lane_w);
+            } else if (L == 32) {  // whole warp: redux.sync (26 cycles on GB300)
                 m = __reduce_max_sync(kFull, k1);
                 win = (int)__reduce_min_sync(kFull, (k1 == m) ? cand : (uint32_t)INT_MAX);
             } else {
