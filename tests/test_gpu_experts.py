@@ -269,3 +269,35 @@ def test_whole_layer(T):
     # E4M3 between the products: 2^-4 of a value or 2^-10 of a group's scale
     # (at most 2^-10 of its largest value / 448); bf16 after each product.
     assert ((y.double() - want).abs() <= size * (2.0 ** -4 + 2.0 ** -8) + want.abs() * 2.0 ** -7 + size.amax() * 2.0 ** -12).all()
+
+
+def test_expert_layer_runs_as_calls_and_as_a_graph():
+    """ExpertLayer: the same bits call by call, on the other buffer set and from
+    a graph; replicas of an expert give what the expert gives."""
+    from combine_moe_plan_gb300 import layer
+    E, P, H, I, k, T = 8, 10, 256, 256, 2, 70
+    ex = layer.random_experts(P, H, I)
+    for t in (ex.w13, ex.s13, ex.w2, ex.s2):  # physical 8 and 9 are second copies of 2 and 5
+        t.view(torch.uint8)[8] = t.view(torch.uint8)[2]
+        t.view(torch.uint8)[9] = t.view(torch.uint8)[5]
+    off = torch.tensor([0, 1, 2, 4, 5, 6, 8, 9, 10], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, 1, 2, 8, 3, 4, 5, 9, 6, 7], dtype=torch.int32, device="cuda")
+    router = moe.Router(n_group=2, topk_group=1, group_top=1)
+    net = layer.ExpertLayer(ex, T, E, k, router, rep_off=off, rep_ids=ids, n_sets=2)
+    g = gen("replicas")
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    y = net(x, logits)
+    assert net.check() == 0
+    assert torch.equal(y, net(x, logits, buf=1))
+    single = layer.ExpertLayer(moe.Experts(ex.w13[:8], ex.s13[:8], ex.w2[:8], ex.s2[:8]), T, E, k, router)
+    assert torch.equal(y, single(x, logits))
+    out = torch.zeros_like(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        net(x, logits, out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, out)
+    with pytest.raises(ValueError):
+        net(x[:5], logits)
