@@ -23,13 +23,12 @@ constexpr int kABytes = kTileM * kGroup;
 constexpr int kBHalf = kGroup * kGroup;
 constexpr int kStageBytes = kABytes + 2 * kBHalf;
 constexpr int kSumWarps = 8;       // warps that scale and add up
-constexpr int kColGroups = kSumWarps / 4;  // warps that share a row
 constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kStoreWarp = kSumWarps + 2;
 constexpr int kExpertsThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
 // 256 x 232 + 128 x 40 = 64,512.
 constexpr int kSumRegs = 232, kOtherRegs = 40;
-constexpr int kHalfN = kGroup / kColGroups;  // columns of each 128-block that a summing warp owns
+constexpr int kHalfN = kGroup / 2;  // columns of each 128-block that a summing warp owns
 
 // The loading thread looks each tile up and leaves it in a ring for the other
 // warps (a lookup costs about 1.5 k cycles of latency, which the summing warps
@@ -37,18 +36,25 @@ constexpr int kHalfN = kGroup / kColGroups;  // columns of each 128-block that a
 // buffers, the accumulators and a staged tile: 4 + 2 + 2 tiles of one block.
 constexpr int kTileRing = 16;
 
-// Finished rows wait in shared memory for the warp that copies them out, so
-// that the summing warps can begin the next tile.  Rows are padded by 16 bytes
-// (no bank conflicts); the pad holds the row's maxima (Up).  The bf16 tile
-// takes the room of one operand buffer: three are enough, for the loads in
-// flight at any time (21 MB over 152 SMs) are several times latency x bandwidth.
+// Finished rows wait in shared memory for the warps that copy them out, so
+// that the summing warps can begin the next tile: columns of 128 bytes by
+// kTileM rows, in the 128-byte swizzle of the boxes that TMA takes them out by
+// (16-byte chunk c of row r lies at c ^ (r mod 8): no bank conflicts when a
+// thread writes its row).  The bf16 tile takes the room of one operand buffer:
+// three are enough, for the loads in flight at any time (21 MB over 152 SMs)
+// are several times latency x bandwidth.
 template <bool UP>
 struct Layout {
-    static constexpr int kStages = UP ? 4 : 3;  // operand buffers
-    static constexpr int kPitch = (UP ? kGroup : 2 * kTileN) + 16;
-    static constexpr int kStagedBytes = kTileM * kPitch;
+    static constexpr int kStages = UP ? 4 : 3;      // operand buffers
+    static constexpr int kOutColumns = UP ? 1 : 4;  // 128-byte columns of a tile's output
+    static constexpr int kStagedBytes = kOutColumns * kTileM * kGroup;
     static constexpr int kBytes = kStages * kStageBytes + kStagedBytes;
 };
+constexpr int kOutBox = 32, kOutBoxSmall = 8;  // rows per TMA box of the output
+
+__device__ __forceinline__ unsigned char* staged_chunk(unsigned char* staged, int column, int row, int chunk) {
+    return staged + (column * kTileM + row) * kGroup + ((chunk ^ (row & 7)) << 4);
+}
 
 struct alignas(16) Barriers {
     uint64_t full[4], empty[4];          // operand buffers
@@ -60,6 +66,7 @@ struct alignas(16) Barriers {
     uint32_t tmem;
     int gave_up;
     int warp_total[kExpertsThreads / 32], warp_top[kExpertsThreads / 32];
+    float maxima[2][kTileM];  // of the two halves of each row (Up)
 };
 
 struct Problem {
@@ -183,8 +190,10 @@ __device__ __forceinline__ float gated(float g, float u) {
 
 template <bool UP>
 __global__ void __launch_bounds__(kExpertsThreads, 1)
-experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const Problem pr) {
-    constexpr int kStages = Layout<UP>::kStages, kPitch = Layout<UP>::kPitch;
+experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out_small,
+               const Problem pr) {
+    constexpr int kStages = Layout<UP>::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t skip = (1024u - (smem_u32(smem) & 1023u)) % 1024u;  // 0 unless the base moved
     unsigned char* stages = smem + skip;
@@ -223,6 +232,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     } else if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_out);
+        tma_prefetch_map(&map_out_small);
     }
     grid_dependency_sync();
     allow_dependents();
@@ -336,33 +347,52 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
         }
         if (warp >= kStoreWarp) {
-            // Copy finished rows out, 16 bytes a lane: 512-byte rows of bf16 by
-            // the whole warp (a single block: half of it idles), 128-byte rows
-            // of codes four at a time.  The two warps take alternate groups.
-            constexpr int kLanes = (UP ? kGroup : 2 * kTileN) / 16, kRows = 32 / kLanes, kBatch = UP ? 4 : 2;
-            const int sub = lane / kLanes, col = (lane % kLanes) * 16;
+            // Copy finished rows out: one thread by TMA, whole boxes of 32 and 8
+            // rows; the other warp the rows left over (a tile ends where its
+            // window ends, and the next row is another expert's), 16 bytes a
+            // lane.  (All rows by the two warps took 8.6 k cycles a bf16 tile,
+            // a bulk copy for each row 11 k.)
+            const int out_columns = Layout<UP>::kOutColumns;
             uint32_t j = 0;
             for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
                 Tile t;
                 if (!__all_sync(kFull, known_tile(j, &t))) break;
-                const bool mine = UP || 2 * t.n + 1 < blocks || col < 2 * kGroup;
-                unsigned char* dst = UP ? pr.h + (size_t)t.n * kGroup + col
-                                        : reinterpret_cast<unsigned char*>(pr.out + (size_t)t.n * kTileN) + col;
-                const size_t pitch = UP ? (size_t)pr.N : 2 * (size_t)pr.N;
+                const int columns = UP || 2 * t.n + 1 < blocks ? out_columns : out_columns / 2;
                 if (!mbar_wait_warp(&b.staged, j & 1, gave_up)) break;
-                for (int r0 = (warp - kStoreWarp) * kBatch * kRows; r0 < t.valid; r0 += 2 * kBatch * kRows) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        v[i] = *reinterpret_cast<const uint4*>(staged + (r0 + i * kRows + sub) * kPitch + col);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i * kRows + sub;
-                        if (mine && r < t.valid) st16(dst + (size_t)(t.row + r) * pitch, v[i]);
+                if (warp == kStoreWarp) {
+                    if (elect_one()) {
+                        const int x0 = t.n * (UP ? kGroup : kTileN);  // elements
+                        for (int c = 0; c < columns; ++c) {
+                            const int x = x0 + c * (UP ? kGroup : kGroup / 2);
+                            const unsigned char* src = staged + c * kTileM * kGroup;
+                            int r = 0;
+                            for (; r + kOutBox <= t.valid; r += kOutBox)
+                                tma_store_2d(&map_out, x, t.row + r, src + r * kGroup);
+                            for (; r + kOutBoxSmall <= t.valid; r += kOutBoxSmall)
+                                tma_store_2d(&map_out_small, x, t.row + r, src + r * kGroup);
+                        }
+                        bulk_commit();
+                        bulk_wait_read();
+                        mbar_arrive(&b.stage_free);
                     }
+                    __syncwarp();
+                } else {
+                    const int from = t.valid & ~(kOutBoxSmall - 1), per_row = columns * 8;
+                    for (int i = lane; i < (t.valid - from) * per_row; i += 32) {
+                        const int r = from + i / per_row, c = i % per_row;
+                        const uint4 v = *reinterpret_cast<const uint4*>(staged_chunk(staged, c >> 3, r, c & 7));
+                        const size_t row = (size_t)(t.row + r) * pr.N;
+                        st16(UP ? static_cast<void*>(pr.h + row + (size_t)t.n * kGroup + 16 * c)
+                                : static_cast<void*>(pr.out + row + (size_t)t.n * kTileN + 8 * c),
+                             v);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.stage_free);
                 }
+            }
+            if (warp == kStoreWarp) {
+                if (elect_one()) bulk_wait();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.stage_free);
             }
         }
     } else {
@@ -431,14 +461,13 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if (lane == 0) mbar_arrive(&b.acc_empty[buf]);
             }
             if (!ok) {
-                if (UP) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");  // let the partner go on
+                if (UP) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // let the partner go on
                 break;
             }
             const Tile now = t;
             const uint32_t parity = j & 1;
             ++j;
             if (tile + gridDim.x < tiles) ok = begin();  // a failure ends the loop after this tile
-            unsigned char* mine = staged + in_tile * kPitch;
             if constexpr (UP) {
                 float amax = 0.0f;
                 if (busy) {
@@ -451,14 +480,13 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
                 // the row's other 64 columns are with the warp 4 further (or back)
-                float* maxima = reinterpret_cast<float*>(mine + kGroup);
                 if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) {
-                    asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");
+                    asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
                     break;
                 }
-                maxima[half] = amax;
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kColGroups) : "memory");
-                for (int i = 0; i < kColGroups; ++i) amax = fmaxf(amax, maxima[i]);
+                b.maxima[half][in_tile] = amax;
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
+                amax = fmaxf(amax, b.maxima[half ^ 1][in_tile]);
                 if (busy) {
                     // a tiny group is scaled up first, so that 448 / amax stays finite
                     const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
@@ -472,7 +500,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                             q[j] = pack_e4m3x2(x.x * lift * inv, x.y * lift * inv) |
                                    pack_e4m3x2(y.x * lift * inv, y.y * lift * inv) << 16;
                         }
-                        st_shared16(mine + half * kHalfN + 16 * i, make_uint4(q[0], q[1], q[2], q[3]));
+                        st_shared16(staged_chunk(staged, 0, in_tile, half * (kHalfN / 16) + i),
+                                    make_uint4(q[0], q[1], q[2], q[3]));
                     }
                     if (half == 0 && in_tile < now.valid)
                         pr.hs[((size_t)now.row + in_tile) * pr.hs_stride + now.n] = amax / kE4M3Max;
@@ -490,12 +519,13 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                                 const float2 x = unpack2(acc[c][4 * i + j]);
                                 q[j] = pack_bf16x2_rn(x.x, x.y);
                             }
-                            st_shared16(mine + 2 * (c * kGroup + half * kHalfN + 8 * i),
+                            st_shared16(staged_chunk(staged, 2 * c + half, in_tile, i),
                                         make_uint4(q[0], q[1], q[2], q[3]));
                         }
                     }
                 }
             }
+            fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.staged);
         }
@@ -533,15 +563,16 @@ EncodeTiledFn encode_tiled() {
     return fn;
 }
 
-// A map of [rows, K] bytes in boxes of box_rows x 128 bytes, 128-byte swizzle;
-// rows past the end read as zero.
-bool byte_map(CUtensorMap* m, const void* base, size_t rows, int K, int box_rows) {
+// A map of a dense [rows, width] tensor of bytes or bf16, in boxes of box_rows x
+// 128 bytes, 128-byte swizzle; a load reads zeros past the end.
+bool tile_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, size_t rows, int width, int box_rows) {
     const EncodeTiledFn encode = encode_tiled();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K};
-    const cuuint32_t box[2] = {kGroup, (cuuint32_t)box_rows}, steps[2] = {1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const int size = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -564,9 +595,14 @@ int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaSt
     // The most row tiles any windows over these rows can have.
     const long long m_most = (long long)(pr.rows + kTileM - 1) / kTileM + min(pr.P, pr.rows);
     if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
-    CUtensorMap map_a, map_w;
-    if (!byte_map(&map_a, a, (size_t)pr.rows, pr.K, kRowBox) ||
-        !byte_map(&map_w, w, (size_t)pr.P * (UP ? 2 : 1) * pr.N, pr.K, kGroup))
+    constexpr CUtensorMapDataType kByte = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    constexpr CUtensorMapDataType kOut = UP ? kByte : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const void* out = UP ? static_cast<const void*>(pr.h) : static_cast<const void*>(pr.out);
+    CUtensorMap map_a, map_w, map_out, map_out_small;
+    if (!tile_map(&map_a, kByte, a, (size_t)pr.rows, pr.K, kRowBox) ||
+        !tile_map(&map_w, kByte, w, (size_t)pr.P * (UP ? 2 : 1) * pr.N, pr.K, kGroup) ||
+        !tile_map(&map_out, kOut, out, (size_t)pr.rows, pr.N, kOutBox) ||
+        !tile_map(&map_out_small, kOut, out, (size_t)pr.rows, pr.N, kOutBoxSmall))
         return MOE_ERR_CUDA;
     const size_t smem = Layout<UP>::kBytes + sizeof(Barriers) + (size_t)(pr.P + 1) * sizeof(int);
     if (cudaFuncSetAttribute(experts_kernel<UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -575,7 +611,8 @@ int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaSt
     const int sms = sm_count();
     if (sms < 1) return MOE_ERR_CUDA;
     const unsigned grid = (unsigned)(m_most * n_tiles < sms ? m_most * n_tiles : sms);
-    return launch_pdl(experts_kernel<UP>, dim3(grid), dim3(kExpertsThreads), smem, s, map_a, map_w, pr) == cudaSuccess
+    return launch_pdl(experts_kernel<UP>, dim3(grid), dim3(kExpertsThreads), smem, s, map_a, map_w, map_out,
+                      map_out_small, pr) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
