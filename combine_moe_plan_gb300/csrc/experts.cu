@@ -125,15 +125,19 @@ struct TileWalk {
 // First row tile of every expert, in shared memory; returns their number.  A
 // window that leaves the rows, runs backwards or starts before an earlier
 // offset (it could share rows with an earlier window) counts as empty and is
-// reported.  Whole CTA.
-__device__ __forceinline__ int scan_windows(const Problem& pr, int* first_m, int* warp_total, int* warp_top) {
+// reported.  The thread that holds the expert of the CTA's first tile leaves
+// that tile in *first (the loading thread need not look it up).  Whole CTA.
+__device__ __forceinline__ int scan_windows(const Problem& pr, int n_tiles, int* first_m, int* warp_total,
+                                            int* warp_top, int4* first) {
     constexpr int kWarps = kExpertsThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (pr.P + kExpertsThreads - 1) / kExpertsThreads;
     const int lo = min(pr.P, (int)threadIdx.x * per), hi = min(pr.P, lo + per);
+    // With an expert a thread at most (P <= 384) its offsets are read once.
+    const int a0 = lo < hi ? pr.offsets[lo] : 0, b0 = lo < hi ? pr.offsets[lo + 1] : 0;
     // the largest offset before this thread's first
-    int top = 0;
-    for (int p = lo; p < hi; ++p) top = max(top, pr.offsets[p]);
+    int top = a0;
+    for (int p = lo + 1; p < hi; ++p) top = max(top, pr.offsets[p]);
     int incl = top;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -148,7 +152,7 @@ __device__ __forceinline__ int scan_windows(const Problem& pr, int* first_m, int
 
     int sum = 0;
     for (int p = lo; p < hi; ++p) {
-        const int a = pr.offsets[p], b = pr.offsets[p + 1];
+        const int a = p == lo ? a0 : pr.offsets[p], b = p == lo ? b0 : pr.offsets[p + 1];
         const bool ok = a >= top && b >= a && b <= pr.rows;
         top = max(top, a);
         if (!ok && blockIdx.x == 0) set_error(pr.err, MOE_DEVERR_WINDOW);
@@ -167,9 +171,15 @@ __device__ __forceinline__ int scan_windows(const Problem& pr, int* first_m, int
     const int mine = lane < kWarps ? warp_total[lane] : 0;
     const int total = __reduce_add_sync(kFull, mine);
     int run = __reduce_add_sync(kFull, lane < warp ? mine : 0) + incl - sum;
+    const int m_first = (int)blockIdx.x / n_tiles;
     for (int p = lo; p < hi; ++p) {
         const int m = first_m[p];
         first_m[p] = run;
+        if (m_first >= run && m_first < run + m) {
+            const int a = p == lo ? a0 : pr.offsets[p], b = p == lo ? b0 : pr.offsets[p + 1];
+            const int local = (int)blockIdx.x - run * n_tiles, n = local / m, row = a + (local - n * m) * kTileM;
+            *first = make_int4(p, n, row, min(kTileM, b - row));
+        }
         run += m;
     }
     if (threadIdx.x == 0) first_m[pr.P] = total;
@@ -237,12 +247,13 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     grid_dependency_sync();
     allow_dependents();
-    const int m_total = scan_windows(pr, first_m, b.warp_total, b.warp_top);  // its barriers publish the above
+    const int blocks = pr.N / kGroup;                       // 128-blocks of outputs
+    const int n_tiles = UP ? blocks : (blocks + 1) / 2;
+    // its barriers publish the above
+    const int m_total = scan_windows(pr, n_tiles, first_m, b.warp_total, b.warp_top, &b.tiles[0]);
     tc_fence_after();
     const uint32_t tmem = b.tmem;
 
-    const int blocks = pr.N / kGroup;                       // 128-blocks of outputs
-    const int n_tiles = UP ? blocks : (blocks + 1) / 2;
     const int width = UP ? 2 * pr.N : pr.N;                 // weight rows per expert
     const int kb = pr.K / kGroup;
     const long long tiles = (long long)m_total * n_tiles;   // at most 2^31: checked by the host
@@ -265,8 +276,15 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             TileWalk walk;
             uint32_t j = 0;
             for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
-                const Tile t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
-                b.tiles[j % kTileRing] = make_int4(t.p, t.n, t.row, t.valid);
+                Tile t;
+                if (j == 0) {
+                    const int4 v = b.tiles[0];
+                    t = {v.x, v.y, v.z, v.w};
+                    walk.p = t.p;
+                } else {
+                    t = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                    b.tiles[j % kTileRing] = make_int4(t.p, t.n, t.row, t.valid);
+                }
                 mbar_arrive(&b.known[j % kTileRing]);
                 const int w0 = t.p * width + (UP ? t.n : 2 * t.n) * kGroup;
                 const bool two = UP || 2 * t.n + 1 < blocks;
