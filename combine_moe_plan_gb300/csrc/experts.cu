@@ -6,6 +6,38 @@
 // 128-element blocks of the inner dimension.  moe_experts_up computes gate and
 // up outputs of the same 128 columns, h = silu(gate) up, and quantizes the 128
 // values of each row as one group; moe_experts_down rounds y to bf16.
+//
+// Mapping.  One persistent CTA per SM walks tiles of 128 rows of one window by
+// two 128-blocks of weight rows.  One thread loads operands by TMA, one issues
+// tcgen05.mma (128 x 256 x 32, E4M3) into two TMEM accumulators, each of one
+// 128-block of the inner dimension: the sum inside a block is the tensor core's,
+// in fp32.  Scales are arbitrary fp32 values per row and block, so a block's
+// sums cannot stay in TMEM: eight warps read them, multiply by sa * sw and add
+// them up in registers (128 a thread).  A thread holds a row, and of it the same
+// 64 columns of both blocks: gate and up meet in one thread, and the row's
+// group maximum takes one exchange with one other warp.  Rows are the M operand
+// whatever their number: an expert with few of them (a decode batch) is bound
+// by its weights' bytes, and its product with 128 mostly empty rows fits into
+// the time that they take to arrive.
+//
+// What bounds it (one GB300, back to back on new inputs).  Few rows an expert:
+// HBM.  96 tokens x 8 over 256 experts of 7168 x 2048 (219 of them chosen, 6.4
+// GB): 927 us, 6.9 TB/s, 1.02 of the measured copy peak.  4096 tokens, 288
+// experts (8.8 GB): 1.35 ms from a cool GPU (0.96), 1.41 to 1.50 ms at its power
+// limit, where the SM clock falls to 1.5 GHz.  Many rows: 98,304 rows over 64
+// experts of 2048 x 1024, first product 336 us cool (2.45 PFLOP/s, 1.27 of the
+// measured bf16 burst), 360 to 380 at the power limit; second 194 to 212.  There
+// a block takes about 850 cycles, of which the product alone needs 543 (alone
+// on the SM; the tensor pipe counts 39 % active) and the multiply-adds 256 of
+// the FMA pipe: the summing warps' own time, wait + read and add (420) + release
+// + loop, is what is left, and reading TMEM is not (loads of 16 columns cost 21
+// cycles one by one and do not slow the product).
+//
+// Measured and left out: 16 summing warps (434 against 402 us at the time);
+// accumulators of 128 columns with two issuing threads (419 / 357); 32 or 64
+// columns a TMEM load (364 / 352); one block of outputs a tile for small batches
+// (one token's second product 27.8 / 26.1 us); row scales loaded four blocks at
+// a time (345 / 336).
 #include <cuda.h>
 
 #include "moe_internal.h"
@@ -209,6 +241,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     unsigned char* stages = smem + skip;
     unsigned char* staged = stages + kStages * kStageBytes;
     Barriers& b = *reinterpret_cast<Barriers*>(stages + Layout<UP>::kBytes);
+    // Room is reserved for an aligned base; another one is refused, not run over.
     if (skip + Layout<UP>::kBytes + sizeof(Barriers) + (pr.P + 1) * sizeof(int) > dynamic_smem_bytes()) {
         if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
         return;
@@ -485,7 +518,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const Tile now = t;
             const uint32_t parity = j & 1;
             ++j;
-            if (tile + gridDim.x < tiles) ok = begin();  // a failure ends the loop after this tile
+            const bool next = tile + gridDim.x >= tiles || begin();
             if constexpr (UP) {
                 float amax = 0.0f;
                 if (busy) {
@@ -546,6 +579,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.staged);
+            ok = next;
         }
         if (!ok && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
         tc_fence_before();
