@@ -48,6 +48,7 @@
 namespace moe {
 namespace {
 
+constexpr int kMostExperts = 4096;
 constexpr int kTileM = 128;        // rows of a tile (TMEM lanes)
 constexpr int kTileN = 256;        // outputs of a tile: two 128-blocks of weight rows
 constexpr int kRowBox = 32;        // rows per TMA box of the row operand
@@ -628,17 +629,15 @@ bool tile_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, size_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// SMs of the current device (0: none).
 int sm_count() {
-    static const int n = [] {
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return 0;
-        }
-        return sms;
-    }();
-    return n;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return sms;
 }
 
 template <bool UP>
@@ -657,7 +656,10 @@ int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaSt
         !tile_map(&map_out_small, kOut, out, (size_t)pr.rows, pr.N, kOutBoxSmall))
         return MOE_ERR_CUDA;
     const size_t smem = Layout<UP>::kBytes + sizeof(Barriers) + (size_t)(pr.P + 1) * sizeof(int);
-    if (cudaFuncSetAttribute(experts_kernel<UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    // The same limit for every P, so that callers on several threads do not lower it for each other.
+    constexpr size_t kMostSmem = Layout<UP>::kBytes + sizeof(Barriers) + (kMostExperts + 1) * sizeof(int);
+    static_assert(kMostSmem <= 227 * 1024, "shared memory of one CTA");
+    if (cudaFuncSetAttribute(experts_kernel<UP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
     const int sms = sm_count();
@@ -673,7 +675,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int check_experts(const moe_experts* e) {
     if (e == nullptr || e->error_word == nullptr) return MOE_ERR_NULL;
-    if (e->P < 1 || e->P > 4096) return MOE_ERR_SIZE;
+    if (e->P < 1 || e->P > kMostExperts) return MOE_ERR_SIZE;
     if (e->H < kGroup || e->H > 65536 || e->H % kGroup != 0) return MOE_ERR_SIZE;
     if (e->I < kGroup || e->I > 65536 || e->I % kGroup != 0) return MOE_ERR_SIZE;
     if (!aligned16(e->error_word)) return MOE_ERR_ALIGN;

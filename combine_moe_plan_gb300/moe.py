@@ -351,22 +351,22 @@ class Experts:
         """h, h_scales = quantised silu(rows gate^T) * (rows up^T) per window."""
         rows = codes.shape[0]
         _tensor("codes", codes, torch.float8_e4m3fn, rows, self.H)
-        _tensor("scales", scales, torch.float32, rows)
+        stride = _tensor("scales", scales, torch.float32, rows)
         self._offsets(offsets)
         _tensor("h", h, torch.float8_e4m3fn, rows, self.I)
-        _tensor("h_scales", h_scales, torch.float32, rows)
-        _call("moe_experts_up", self._ref, codes.data_ptr(), scales.data_ptr(), scales.shape[1], offsets.data_ptr(),
-              rows, h.data_ptr(), h_scales.data_ptr(), h_scales.shape[1], _stream(stream))
+        h_stride = _tensor("h_scales", h_scales, torch.float32, rows)
+        _call("moe_experts_up", self._ref, codes.data_ptr(), scales.data_ptr(), stride, offsets.data_ptr(),
+              rows, h.data_ptr(), h_scales.data_ptr(), h_stride, _stream(stream))
         return h, h_scales
 
     def down(self, h, h_scales, offsets, out, stream=None):
         """out = bf16(h w2^T) per window."""
         rows = h.shape[0]
         _tensor("h", h, torch.float8_e4m3fn, rows, self.I)
-        _tensor("h_scales", h_scales, torch.float32, rows)
+        stride = _tensor("h_scales", h_scales, torch.float32, rows)
         self._offsets(offsets)
         _tensor("out", out, torch.bfloat16, rows, self.H)
-        _call("moe_experts_down", self._ref, h.data_ptr(), h_scales.data_ptr(), h_scales.shape[1],
+        _call("moe_experts_down", self._ref, h.data_ptr(), h_scales.data_ptr(), stride,
               offsets.data_ptr(), rows, out.data_ptr(), _stream(stream))
         return out
 
@@ -382,11 +382,13 @@ class Experts:
 
 def _tensor(name, t, dtype, rows, width=None):
     """A dense two-dimensional tensor of this type, with at least ``rows`` rows
-    of ``width`` elements (None: any)."""
-    if t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or t.shape[0] < rows or \
-            (width is not None and t.shape[1] != width):
+    of ``width`` elements (None: any); returns its width."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 2 or shape[0] < rows or (width is not None and shape[1] != width) or \
+            not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous {dtype} tensor of at least {rows} rows of "
-                         f"{'any width' if width is None else width}, got {t.dtype} {tuple(t.shape)}")
+                         f"{'any width' if width is None else width}, got {t.dtype} {tuple(shape)}")
+    return shape[1]
 
 
 def _block_scaled(name, w, s, P, n, k):

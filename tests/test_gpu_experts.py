@@ -162,11 +162,36 @@ def test_no_rows_at_all():
     assert ex.check() == 0
 
 
-def test_many_experts():
-    rng = np.random.default_rng(5)
-    sizes = list(rng.integers(0, 4, 600))
+@pytest.mark.parametrize("P", [383, 384, 385, 600, 4096])
+def test_many_experts(P):
+    """One expert a thread, several, and the most there may be."""
+    rng = np.random.default_rng(P)
+    sizes = list(rng.integers(0, 4, P))
     check_down(sizes, 128, 128)
     check_up(sizes, 128, 128)
+
+
+def test_several_threads():
+    """Calls of different sizes from four host threads on their own streams."""
+    import threading
+    jobs = [(check_down, [30, 0, 200], 384, 256), (check_up, [1] * 500, 128, 128), (check_down, [3] * 700, 128, 128),
+            (check_up, [129, 64], 256, 640)]
+    failed = []
+
+    def work(job):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3):
+                    job[0](*job[1:])
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
 
 
 def test_bad_windows_are_skipped_and_reported():
