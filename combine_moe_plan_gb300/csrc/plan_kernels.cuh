@@ -708,7 +708,7 @@ cudaError_t launch_plan_with(R router, const float* logits, int T, int E, int P,
     // Three launches.  Lanes per token: route_lanes; tokens per tile:
     // route_tile_tokens (16 for mid-size batches of whole-warp tokens).  The
     // tile-count scratch has route_tiles(T) columns.
-    const int L = router.whole_warps() ? 32 : route_lanes(E, k);
+    const int L = router.whole_warps(E) ? 32 : route_lanes(E, k);
     const int tt = route_tile_tokens(T, E, k);
     const int tiles = (T + tt - 1) / tt;
     const size_t rsmem = route_smem(tt, E, P, k);

@@ -142,7 +142,7 @@ __device__ __forceinline__ float tile_gate(int T, int k, int t0, const float* se
 // selected ones (tile_gate).
 struct TopkSoftmax {
     static constexpr bool kScored = false;
-    static bool whole_warps() { return false; }
+    static bool whole_warps(int) { return false; }
 };
 
 // moe_plan_routed's router.  Every quantity is binary32:
@@ -163,8 +163,13 @@ struct ScoreRouter {
     bool sigmoid;
     int n_group, topk_group, group_top;
     bool renorm;
-    // Groups are compared across a whole warp (one lane per group).
-    bool whole_warps() const { return n_group > 1; }
+    // Whether the three-launch plan gives a token a whole warp whatever
+    // route_lanes says.  Groups are compared across one (a lane a group); and
+    // with the ballot in place of a second reduction a whole warp's rounds are
+    // the shorter ones from 32 experts on (16384 tokens: 64 experts, top-6 16.6
+    // us against 20.7 with 8 lanes; 32 experts, top-4 12.6 / 12.8; 16 experts
+    // 12.4 / 10.5; 4096 tokens, 128 experts, top-8 9.5 / 19.3 with 16 lanes).
+    bool whole_warps(int E) const { return n_group > 1 || E > 16; }
 
     // NaN (a NaN logit, or a row without a finite logit) counts as score 0.
     __device__ __forceinline__ float score(float l, float2 stat) const {

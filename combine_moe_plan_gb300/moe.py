@@ -126,10 +126,15 @@ def header_functions(path: str = HEADER) -> list[str]:
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != MOE_OK:
         raise MoeError(name, rc, lib().moe_status_str(rc).decode())
     return rc
+
+
+# The pair torch.cuda.current_stream() itself reads (a torch without CUDA has neither).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _ptr(t):
@@ -140,7 +145,7 @@ def _stream(stream):
     """The stream's handle; without one the current stream's, read without
     building a torch Stream (2.8 us of a call that takes 2.5 us itself)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device())
     return stream.cuda_stream
 
 
