@@ -67,9 +67,11 @@ namespace {
 // the other buffer set could share that SM; with half the file left free the
 // pipelined step is about 2.5 us shorter at 4096 tokens and the plan alone no
 // slower.  Smaller CTAs (8 or 16 lanes a token, for small expert counts) take
-// a quarter or half of that register file.
+// a quarter or half of that register file.  The scored router with 8 lanes a
+// token has twice the registers (16384 tokens, 8 experts: 6.0 us against 7.4);
+// with a whole warp a token it is the faster for the cap (64 experts 14.3 / 17.6).
 template <int EPL, int THREADS, int TT, class R>
-__global__ void __launch_bounds__(THREADS, 2048 / THREADS)
+__global__ void __launch_bounds__(THREADS, (R::kScored && THREADS == 256 ? 1024 : 2048) / THREADS)
 route_tile_kernel(R router, const float* __restrict__ logits, int T, int E, int P, int k,
                   const int32_t* __restrict__ rep_off, const int32_t* __restrict__ rep_ids,
                   int32_t* __restrict__ topk_e, float* __restrict__ gates,
