@@ -69,7 +69,8 @@ namespace {
 // slower.  Smaller CTAs (8 or 16 lanes a token, for small expert counts) take
 // a quarter or half of that register file.  The scored router with 8 lanes a
 // token has twice the registers (16384 tokens, 8 experts: 6.0 us against 7.4);
-// with a whole warp a token it is the faster for the cap (64 experts 14.3 / 17.6).
+// with a whole warp a token it is the faster for the cap (16384 tokens, 64
+// experts: 14.3 / 17.6).
 template <int EPL, int THREADS, int TT, class R>
 __global__ void __launch_bounds__(THREADS, (R::kScored && THREADS == 256 ? 1024 : 2048) / THREADS)
 route_tile_kernel(R router, const float* __restrict__ logits, int T, int E, int P, int k,
@@ -710,7 +711,7 @@ cudaError_t launch_plan_with(R router, const float* logits, int T, int E, int P,
     // Three launches.  Lanes per token: route_lanes; tokens per tile:
     // route_tile_tokens (16 for mid-size batches of whole-warp tokens).  The
     // tile-count scratch has route_tiles(T) columns.
-    const int L = router.whole_warps(E) ? 32 : route_lanes(E, k);
+    const int L = router.whole_warps(T, E) ? 32 : route_lanes(E, k);
     const int tt = route_tile_tokens(T, E, k);
     const int tiles = (T + tt - 1) / tt;
     const size_t rsmem = route_smem(tt, E, P, k);

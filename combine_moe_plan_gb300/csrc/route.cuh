@@ -142,7 +142,7 @@ __device__ __forceinline__ float tile_gate(int T, int k, int t0, const float* se
 // selected ones (tile_gate).
 struct TopkSoftmax {
     static constexpr bool kScored = false;
-    static bool whole_warps(int) { return false; }
+    static bool whole_warps(int, int) { return false; }
 };
 
 // moe_plan_routed's router.  Every quantity is binary32:
@@ -164,12 +164,17 @@ struct ScoreRouter {
     int n_group, topk_group, group_top;
     bool renorm;
     // Whether the three-launch plan gives a token a whole warp whatever
-    // route_lanes says.  Groups are compared across one (a lane a group); and
-    // with the ballot in place of a second reduction a whole warp's rounds are
-    // the shorter ones from 32 experts on (16384 tokens: 64 experts, top-6 16.6
-    // us against 20.7 with 8 lanes; 32 experts, top-4 12.6 / 12.8; 16 experts
-    // 12.4 / 10.5; 4096 tokens, 128 experts, top-8 9.5 / 19.3 with 16 lanes).
-    bool whole_warps(int E) const { return n_group > 1 || E > 16; }
+    // route_lanes says.  Groups are compared across one (a lane a group).
+    // Above 64 experts its rounds, with a ballot in place of a second
+    // reduction, are the shorter ones (4096 tokens, 128 experts, top-8: 9.5 us
+    // against 19.3 with 16 lanes); from 17 to 64 as long as every tile has an SM
+    // to itself (64 experts, top-6: 2048 tokens 7.8 us against 8.8 with 8 lanes,
+    // 4096 8.0 / 9.1, but 12288 13.7 / 12.1, 16384 16.6 / 14.1); below that 8
+    // lanes do (16384 tokens, 16 experts: 7.9 against 12.4).
+    bool whole_warps(int T, int E) const {
+        constexpr int kTilePerSm = 152 * kTileTokens;  // tokens
+        return n_group > 1 || E > 64 || (E > 16 && T <= kTilePerSm);
+    }
 
     // NaN (a NaN logit, or a row without a finite logit) counts as score 0.
     __device__ __forceinline__ float score(float l, float2 stat) const {

@@ -131,6 +131,14 @@ def test_batch_sizes_without_groups(T, E, k):
     check(logits, (rng.integers(-50, 50, E) / 1000).astype(np.float32), k, score="softmax", renorm=False, scale=0.5)
 
 
+@pytest.mark.parametrize("T", [4864, 4865])
+@pytest.mark.parametrize("E,k", [(16, 3), (17, 4), (64, 6), (65, 8)])
+def test_large_batches(T, E, k):
+    """Both sides of the limits between 8 lanes and a warp a token."""
+    rng = np.random.default_rng([T, E, 1])
+    check(grid_logits(rng, T, E), (rng.integers(-50, 50, E) / 1000).astype(np.float32), k, score="softmax", scale=2.0)
+
+
 @pytest.mark.parametrize("T", [3, 700])
 def test_replicas(T):
     rng = np.random.default_rng(T)
