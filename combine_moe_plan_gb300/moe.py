@@ -179,6 +179,7 @@ class Pool:
         h = ctypes.c_void_p()
         _call("moe_pool_init", ctypes.byref(self.desc), _ptr(self.workspace), self.nbytes, ctypes.byref(h))
         self.handle = h
+        self._views = {}
         _call("moe_pool_clear_error", self.handle, _stream(stream))
 
     def __del__(self):
@@ -240,9 +241,11 @@ class Pool:
         """The set's rows (after ``dispatch_f8``) through ``experts``: their
         gated product into ``h`` / ``h_scales`` (``Experts.inner(rows)``), then
         their down projection into the set's ex_out, ready for ``combine``."""
-        v, n = self.view(buf), T * self.k
-        experts.up(v["codes_f8"][:n], v["scales"][:n], v["offsets"], h, h_scales, stream=stream)
-        experts.down(h[:n], h_scales[:n], v["offsets"], v["ex_out"][:n], stream=stream)
+        if buf not in self._views:  # a set's buffers never move
+            self._views[buf] = self.view(buf)
+        v, n = self._views[buf], T * self.k
+        experts.up(v["codes_f8"], v["scales"], v["offsets"], h, h_scales, rows=n, stream=stream)
+        experts.down(h, h_scales, v["offsets"], v["ex_out"], rows=n, stream=stream)
 
     def dispatch(self, x, buf=0, stream=None, after_plan=False):
         """moe_dispatch; with ``after_plan`` moe_dispatch_after_plan, which
@@ -352,9 +355,10 @@ class Experts:
         return (torch.empty((rows, self.I), dtype=torch.float8_e4m3fn, device=dev),
                 torch.zeros((rows, (self.I // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
 
-    def up(self, codes, scales, offsets, h, h_scales, stream=None):
-        """h, h_scales = quantised silu(rows gate^T) * (rows up^T) per window."""
-        rows = codes.shape[0]
+    def up(self, codes, scales, offsets, h, h_scales, rows=None, stream=None):
+        """h, h_scales = quantised silu(rows gate^T) * (rows up^T) per window;
+        the windows lie in the first ``rows`` rows (None: all of ``codes``)."""
+        rows = codes.shape[0] if rows is None else rows
         _tensor("codes", codes, torch.float8_e4m3fn, rows, self.H)
         stride = _tensor("scales", scales, torch.float32, rows)
         self._offsets(offsets)
@@ -364,9 +368,9 @@ class Experts:
               rows, h.data_ptr(), h_scales.data_ptr(), h_stride, _stream(stream))
         return h, h_scales
 
-    def down(self, h, h_scales, offsets, out, stream=None):
-        """out = bf16(h w2^T) per window."""
-        rows = h.shape[0]
+    def down(self, h, h_scales, offsets, out, rows=None, stream=None):
+        """out = bf16(h w2^T) per window; ``rows`` as in ``up``."""
+        rows = h.shape[0] if rows is None else rows
         _tensor("h", h, torch.float8_e4m3fn, rows, self.I)
         stride = _tensor("h_scales", h_scales, torch.float32, rows)
         self._offsets(offsets)
