@@ -600,6 +600,11 @@ cudaError_t launch_cluster(R router, const float* logits, int T, int E, int P, i
         (e = cudaFuncSetAttribute(plan_cluster_kernel<EPL, TT, R>, cudaFuncAttributeNonPortableClusterSizeAllowed,
                                   1)) != cudaSuccess)
         return e;
+    // A cluster of one needs no cluster launch (0.15 to 0.3 us less).
+    if (n_tiles == 1)
+        return launch_pdl_at(urgent, plan_cluster_kernel<EPL, TT, R>, dim3(1), dim3(32 * TT), smem1, s, router, logits,
+                             T, E, P, k, rep_off, rep_ids, topk_e, gates, phys, counts, offsets, slot, src_token, src_k,
+                             err);
     return launch_pdl_cluster(urgent, (unsigned)n_tiles, plan_cluster_kernel<EPL, TT, R>, dim3(n_tiles),
                               dim3(32 * TT), smem1, s, router, logits, T, E, P, k, rep_off, rep_ids, topk_e, gates, phys,
                               counts, offsets, slot, src_token, src_k, err);
