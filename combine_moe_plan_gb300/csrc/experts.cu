@@ -291,13 +291,14 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int width = UP ? 2 * pr.N : pr.N;                 // weight rows per expert
     const int kb = pr.K / kGroup;
     const long long tiles = (long long)m_total * n_tiles;   // at most 2^31: checked by the host
-    // Tile number j of this CTA, once the loading thread has left it in the ring.
-    const auto known_tile = [&](uint32_t j, Tile* t) {
+    // Tile number j of this CTA, once the loading thread has left it in the
+    // ring.  After a wait has given up: an empty tile, so that every warp still
+    // passes the same barriers to the end.
+    const auto known_tile = [&](uint32_t j) {
         const int i = j % kTileRing;
-        if (!mbar_wait(&b.known[i], (j / kTileRing) & 1, gave_up)) return false;
+        if (!mbar_wait(&b.known[i], (j / kTileRing) & 1, gave_up)) return Tile{0, 0, 0, 0};
         const int4 v = *const_cast<const int4*>(&b.tiles[i]);
-        *t = {v.x, v.y, v.z, v.w};
-        return true;
+        return Tile{v.x, v.y, v.z, v.w};
     };
 
     if (warp >= kSumWarps) {
@@ -352,7 +353,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 set_error(pr.err, MOE_DEVERR_STALL);
                 const uint64_t t0 = now_ns();
                 for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    while (!mbar_try(&b.full[i % kStages], (i / kStages) & 1) && now_ns() - t0 < kStallNs) {
+                    while (!mbar_try(smem_u32(&b.full[i % kStages]), (i / kStages) & 1) && now_ns() - t0 < kStallNs) {
                     }
             }
         }
@@ -363,9 +364,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const uint64_t desc_a = umma_desc(stages), desc_w = umma_desc(stages + kABytes);
             uint32_t j = 0;
             for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
-                Tile t;
-                if (!UP && !(ok = known_tile(j, &t))) break;
-                const bool two = UP || 2 * t.n + 1 < blocks;
+                const bool two = UP || 2 * known_tile(j).n + 1 < blocks;
                 const uint32_t idesc = umma_idesc_e4m3(kTileM, two ? kTileN : kGroup);
                 for (int k = 0; k < kb; ++k, ++it) {
                     const uint32_t buf = it & 1;
@@ -394,7 +393,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 set_error(pr.err, MOE_DEVERR_STALL);
                 umma_commit(&b.drain);
                 const uint64_t t0 = now_ns();
-                while (!mbar_try(&b.drain, 0) && now_ns() - t0 < kStallNs) {
+                while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
                 }
             }
         }
@@ -407,10 +406,9 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const int out_columns = Layout<UP>::kOutColumns;
             uint32_t j = 0;
             for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
-                Tile t;
-                if (!__all_sync(kFull, known_tile(j, &t))) break;
+                const Tile t = known_tile(j);
                 const int columns = UP || 2 * t.n + 1 < blocks ? out_columns : out_columns / 2;
-                if (!mbar_wait_warp(&b.staged, j & 1, gave_up)) break;
+                mbar_pass(smem_u32(&b.staged), j & 1, gave_up);
                 if (warp == kStoreWarp) {
                     if (elect_one()) {
                         const int x0 = t.n * (UP ? kGroup : kTileN);  // elements
@@ -454,8 +452,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t my_tmem = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalfN;
         const int in_tile = quarter * 32 + lane;
-        uint32_t it = 0, j = 0;
-        bool ok = true;
+        uint32_t j = 0;
         Tile t = {0, 0, 0, 0};
         const float *sa = nullptr, *sw = nullptr;  // scales of the row and of the first 128-block
         int gap = 0;                               // from there to the second block's
@@ -463,35 +460,46 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         // Tile j and its first scales: loaded before the tile in front of it is
         // finished and stored, and needed after.
         const auto begin = [&]() {
-            if (!__all_sync(kFull, known_tile(j, &t))) return false;
-            sa = pr.sa + ((size_t)t.row + min(in_tile, t.valid - 1)) * pr.sa_stride;
+            t = known_tile(j);
+            __syncwarp();
+            sa = pr.sa + ((size_t)t.row + max(0, min(in_tile, t.valid - 1))) * pr.sa_stride;
             const int blk = UP ? t.n : 2 * t.n;
             sw = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
             gap = UP ? blocks * kb : (blk + 1 < blocks ? kb : 0);
             ar = __ldg(sa);
             f0 = __ldg(sw);
             f1 = __ldg(sw + gap);
-            return true;
         };
-        if (blockIdx.x < tiles) ok = begin();
-        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        if (blockIdx.x < tiles) begin();
+        // The two accumulators in turn: `buf` 0 or 1, `phase` the parity of their
+        // barriers' phases, which flips after both.
+        const uint32_t full_bar = smem_u32(&b.acc_full[0]), empty_bar = smem_u32(&b.acc_empty[0]);
+        uint32_t buf = 0, phase = 0;
+        // The accumulator is read: it may be written again.
+        const auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(empty_bar + 8 * buf);
+        };
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
             uint64_t acc[2][kHalfN / 2];
 #pragma unroll
             for (int i = 0; i < kHalfN / 2; ++i) acc[0][i] = acc[1][i] = 0ull;
-            for (int k = 0; k < kb; ++k, ++it) {
-                const uint32_t buf = it & 1;
+            // This loop is the compute-bound products' critical path, and every
+            // instruction in it counts: unrolled four times, with constant
+            // buffers and offsets, it is 25 % slower.
+#pragma unroll 1
+            for (int k = 0; k < kb; ++k) {
                 const float s0 = ar * f0, s1 = ar * f1;
                 if (k + 1 < kb) {  // the next block's scales, a block ahead
                     ar = __ldg(sa + k + 1);
                     f0 = __ldg(sw + k + 1);
                     f1 = __ldg(sw + gap + k + 1);
                 }
-                if (!(ok = mbar_wait_warp(&b.acc_full[buf], (it >> 1) & 1, gave_up))) break;
+                mbar_pass(full_bar + 8 * buf, phase, gave_up);
                 tc_fence_after();
                 if (busy) {
-                    const uint64_t s2[2] = {pack2(__float_as_uint(s0), __float_as_uint(s0)),
-                                            pack2(__float_as_uint(s1), __float_as_uint(s1))};
                     const uint32_t base = my_tmem + buf * kTileN;
                     uint32_t v[2][16];
                     tmem_load16(base, v[0]);
@@ -501,25 +509,25 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         if (c + 1 < 2 * kHalfN / 16)
                             tmem_load16(base + ((c + 1) / (kHalfN / 16)) * kGroup + ((c + 1) % (kHalfN / 16)) * 16,
                                         v[(c + 1) & 1]);
-                        const int blkc = c / (kHalfN / 16), c0 = (c % (kHalfN / 16)) * 8;
+                        else
+                            release();
+                        const int h = c / (kHalfN / 16), c0 = (c % (kHalfN / 16)) * 8;
+                        const uint32_t f = __float_as_uint(h == 0 ? s0 : s1);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            acc[blkc][c0 + i] = fma2(pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2[blkc],
-                                                     acc[blkc][c0 + i]);
+                            acc[h][c0 + i] =
+                                fma2(pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), pack2(f, f), acc[h][c0 + i]);
                     }
+                } else {
+                    release();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.acc_empty[buf]);
-            }
-            if (!ok) {
-                if (UP) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // let the partner go on
-                break;
+                phase ^= buf;
+                buf ^= 1;
             }
             const Tile now = t;
             const uint32_t parity = j & 1;
             ++j;
-            const bool next = tile + gridDim.x >= tiles || begin();
+            if (tile + gridDim.x < tiles) begin();
             if constexpr (UP) {
                 float amax = 0.0f;
                 if (busy) {
@@ -532,10 +540,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
                 // the row's other 64 columns are with the warp 4 further (or back)
-                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) {
-                    asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
-                    break;
-                }
+                mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
                 b.maxima[half][in_tile] = amax;
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
                 amax = fmaxf(amax, b.maxima[half ^ 1][in_tile]);
@@ -559,7 +564,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         pr.hs[((size_t)now.row + in_tile) * pr.hs_stride + now.n] = amax / kE4M3Max;
                 }
             } else {
-                if (!(ok = mbar_wait_warp(&b.stage_free, parity ^ 1, gave_up))) break;
+                mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
                 if (busy) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -580,9 +585,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.staged);
-            ok = next;
         }
-        if (!ok && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
+        if (*gave_up && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
         tc_fence_before();
     }
     __syncthreads();
