@@ -23,14 +23,14 @@
 // What bounds it (one GB300, back to back on new inputs).  Few rows an expert:
 // HBM.  96 tokens x 8 over 256 experts of 7168 x 2048 (219 of them chosen, 6.4
 // GB): 927 us, 6.9 TB/s, 1.02 of the measured copy peak.  4096 tokens, 288
-// experts (8.8 GB): 1.35 ms from a cool GPU (0.96), 1.41 to 1.50 ms at its power
+// experts (8.8 GB): 1.31 ms from a cool GPU (0.98), 1.41 to 1.47 ms at its power
 // limit, where the SM clock falls to 1.5 GHz.  Many rows: 98,304 rows over 64
-// experts of 2048 x 1024, first product 336 us cool (2.45 PFLOP/s, 1.27 of the
-// measured bf16 burst), 360 to 380 at the power limit; second 194 to 212.  There
-// a block takes about 850 cycles, of which the product alone needs 543 (alone
-// on the SM; the tensor pipe counts 39 % active) and the multiply-adds 256 of
-// the FMA pipe: the summing warps' own time, wait + read and add (420) + release
-// + loop, is what is left, and reading TMEM is not (loads of 16 columns cost 21
+// experts of 2048 x 1024, first product 316 us cool (2.6 PFLOP/s, 1.35 of the
+// measured bf16 burst), 366 at the power limit; second 191 and 212.  There a
+// block takes about 790 cycles, of which the product alone needs 543 (alone on
+// the SM; the tensor pipe counts 42 % active) and the multiply-adds 256 of the
+// FMA pipe: the summing warps' own time, wait + read and add (420) + release +
+// loop, is what is left, and reading TMEM is not (loads of 16 columns cost 21
 // cycles one by one and do not slow the product).
 //
 // Measured and left out: 16 summing warps (434 against 402 us at the time);
