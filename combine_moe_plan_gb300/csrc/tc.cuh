@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <cuda.h>  // CUtensorMap
 
+#include "wait.h"
+
 namespace moe {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -36,11 +38,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Every wait looks once (54 cycles) before it polls in a way that may sleep (86
-// where the phase is over already): most phases a warp waits for are over, and
-// the look is on its way from block to block (first product of 98,304 rows 325
-// us against 338 without).
-constexpr uint32_t kPollNs = 1000000;  // a poll may sleep this long; it wakes when the phase ends
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -67,46 +64,34 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Waits are bounded: a wait that is not over after kStallTries polls (tens of
-// microseconds) starts a clock, and gives up kStallNs later; it then tells the
-// CTA's other waits through *gave_up and returns false.  The clock is not read
-// before that: reading %globaltimer takes several hundred cycles, which every
-// wait that is not over at its first poll would pay.
-constexpr uint64_t kStallNs = 4000000000ull;
-constexpr int kStallTries = 4096;
-
 __device__ __forceinline__ uint64_t now_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
 
-// Polls on with the clock running; true once the wait has to be given up.
-__device__ __forceinline__ bool mbar_stalled(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    for (const uint64_t t0 = now_ns();;) {
-        if (mbar_try(bar, parity)) return false;
-        if (*gave_up) return true;
-        if (now_ns() - t0 > kStallNs) {
-            *gave_up = 1;
-            return true;
-        }
-    }
-}
+// A phase of an mbarrier, for the bounded wait of wait.h.  The look takes 54
+// cycles and the poll 86 where the phase is over already; most phases a warp
+// waits for are, and the look is on its way from block to block (first product
+// of 98,304 rows 325 us against 338 without).
+struct MbarPhase {
+    uint32_t bar, parity;
+    __device__ __forceinline__ bool over() const { return mbar_test(bar, parity); }
+    __device__ __forceinline__ bool poll() const { return mbar_try(bar, parity); }
+    __device__ __forceinline__ uint64_t now() const { return now_ns(); }
+};
+
+// Wait for a phase; false once this wait or another of the CTA has given up.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    const uint32_t at = smem_u32(bar);
-    if (mbar_test(at, parity)) return true;
-    for (int i = 0; i < kStallTries; ++i)
-        if (mbar_try(at, parity)) return true;
-    return !mbar_stalled(at, parity, gave_up);
+    return wait_bounded(MbarPhase{smem_u32(bar), parity}, gave_up);
 }
 
 // For the warps that hold no copies in flight: once a wait has given up they run
-// on without waiting (their results are void, and reported so), which keeps
-// branches out of their loops.  Whole warp; `bar` as a shared-memory address.
+// on, each later wait taking one poll at most (their results are void, and
+// reported so), which keeps branches out of their loops.  Whole warp; `bar` as a shared-memory
+// address.
 __device__ __forceinline__ void mbar_pass(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    if (!mbar_test(bar, parity))
-        for (int i = 0; !mbar_try(bar, parity); ++i)
-            if (i >= kStallTries && mbar_stalled(bar, parity, gave_up)) break;
+    (void)wait_bounded(MbarPhase{bar, parity}, gave_up);
     __syncwarp();
 }
 
