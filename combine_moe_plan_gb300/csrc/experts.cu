@@ -292,13 +292,22 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int kb = pr.K / kGroup;
     const long long tiles = (long long)m_total * n_tiles;   // at most 2^31: checked by the host
     // Tile number j of this CTA, once the loading thread has left it in the
-    // ring.  After a wait has given up: an empty tile, so that every warp still
+    // ring (wait_written: never an entry that it has not written).
+    const auto tile_written = [&](uint32_t j) {
+        return wait_written(MbarPhase{smem_u32(&b.known[j % kTileRing]), (j / kTileRing) & 1}, gave_up);
+    };
+    const auto tile_at = [&](uint32_t j) {
+        const int4 v = *const_cast<const int4*>(&b.tiles[j % kTileRing]);
+        return Tile{v.x, v.y, v.z, v.w};
+    };
+    // For a whole warp, the same answer in every lane (its TMEM loads and
+    // barriers are the whole warp's).  After a wait has given up: an empty tile,
+    // for which the warp sums, waits for and stores nothing, so that it still
     // passes the same barriers to the end.
     const auto known_tile = [&](uint32_t j) {
-        const int i = j % kTileRing;
-        if (!mbar_wait(&b.known[i], (j / kTileRing) & 1, gave_up)) return Tile{0, 0, 0, 0};
-        const int4 v = *const_cast<const int4*>(&b.tiles[i]);
-        return Tile{v.x, v.y, v.z, v.w};
+        const bool written = tile_written(j);
+        const Tile t = tile_at(j);  // on its way while the lanes agree
+        return __all_sync(kFull, written) ? t : Tile{0, 0, 0, 0};
     };
 
     if (warp >= kSumWarps) {
@@ -310,7 +319,10 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             bool ok = true;
             TileWalk walk;
             uint32_t j = 0;
-            for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+                // no tile is written any more, so none overwrites one that a
+                // warp which runs on without waiting is reading
+                if (!(ok = ok && *gave_up == 0)) break;
                 Tile t;
                 if (j == 0) {
                     const int4 v = b.tiles[0];
@@ -364,7 +376,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const uint64_t desc_a = umma_desc(stages), desc_w = umma_desc(stages + kABytes);
             uint32_t j = 0;
             for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
-                const bool two = UP || 2 * known_tile(j).n + 1 < blocks;
+                if (!UP && !(ok = tile_written(j))) break;
+                const bool two = UP || 2 * tile_at(j).n + 1 < blocks;
                 const uint32_t idesc = umma_idesc_e4m3(kTileM, two ? kTileN : kGroup);
                 for (int k = 0; k < kb; ++k, ++it) {
                     const uint32_t buf = it & 1;
@@ -408,7 +421,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
                 const Tile t = known_tile(j);
                 const int columns = UP || 2 * t.n + 1 < blocks ? out_columns : out_columns / 2;
-                mbar_pass(smem_u32(&b.staged), j & 1, gave_up);
+                if (t.valid > 0) mbar_pass(smem_u32(&b.staged), j & 1, gave_up);
                 if (warp == kStoreWarp) {
                     if (elect_one()) {
                         const int x0 = t.n * (UP ? kGroup : kTileN);  // elements
@@ -461,7 +474,6 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         // finished and stored, and needed after.
         const auto begin = [&]() {
             t = known_tile(j);
-            __syncwarp();
             sa = pr.sa + ((size_t)t.row + max(0, min(in_tile, t.valid - 1))) * pr.sa_stride;
             const int blk = UP ? t.n : 2 * t.n;
             sw = pr.sw + ((size_t)t.p * (width / kGroup) + blk) * kb;
@@ -483,6 +495,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         };
         for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const bool busy = quarter * 32 < t.valid;  // the warp holds a row of the window
+            const int steps = t.valid > 0 ? kb : 0;
             uint64_t acc[2][kHalfN / 2];
 #pragma unroll
             for (int i = 0; i < kHalfN / 2; ++i) acc[0][i] = acc[1][i] = 0ull;
@@ -490,7 +503,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             // instruction in it counts: unrolled four times, with constant
             // buffers and offsets, it is 25 % slower.
 #pragma unroll 1
-            for (int k = 0; k < kb; ++k) {
+            for (int k = 0; k < steps; ++k) {
                 const float s0 = ar * f0, s1 = ar * f1;
                 if (k + 1 < kb) {  // the next block's scales, a block ahead
                     ar = __ldg(sa + k + 1);
@@ -540,7 +553,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
                 // the row's other 64 columns are with the warp 4 further (or back)
-                mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
+                if (now.valid > 0) mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
                 b.maxima[half][in_tile] = amax;
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
                 amax = fmaxf(amax, b.maxima[half ^ 1][in_tile]);
@@ -564,7 +577,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         pr.hs[((size_t)now.row + in_tile) * pr.hs_stride + now.n] = amax / kE4M3Max;
                 }
             } else {
-                mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
+                if (now.valid > 0) mbar_pass(smem_u32(&b.stage_free), parity ^ 1, gave_up);
                 if (busy) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {

@@ -44,4 +44,14 @@ MOE_WAIT_FN bool wait_bounded(const Phase& phase, volatile int* gave_up) {
     }
 }
 
+// Wait until an entry of a ring is written: `phase` is that of the entry's
+// barrier, whose parity stands for its uses in turn.  After a wait has given up
+// the writer may have stopped anywhere, and the parity of a barrier that has been
+// left behind says "over" again one round of the ring later, for an entry that
+// was never written; so nothing counts as written from then on (and nothing is polled for).
+template <class Phase>
+MOE_WAIT_FN bool wait_written(const Phase& phase, volatile int* gave_up) {
+    return (phase.over() || (*gave_up == 0 && wait_bounded(phase, gave_up))) && *gave_up == 0;
+}
+
 }  // namespace moe

@@ -66,3 +66,14 @@ def test_a_phase_that_ends(model):
         assert r["ok"] == 1 and r["reads"] == 0 and r["ns"] <= ends + 45
     r = run(model, ends=model.wait_limit_ns() // 2)
     assert r["ok"] == 1 and r["ns"] <= model.wait_limit_ns() // 2 + 400
+
+
+@pytest.mark.parametrize("written", [0, 1, 5, 15, 16, 17, 40, 64])
+def test_only_written_ring_entries_count(model, written):
+    """A reader of a ring whose writer has stopped takes the entries it wrote and
+    no other, also a round later, when the parity of a barrier that was left
+    behind says "over" again."""
+    n = 100
+    ok = (ctypes.c_ubyte * n)()
+    model.ring_run(16, written, n, ok)
+    assert list(ok) == [1] * written + [0] * (n - written)

@@ -38,6 +38,21 @@ struct Phase {
     }
 };
 
+// An mbarrier of a ring entry that has been written `uses` times: its current
+// phase is number `uses`, and a wait on a parity is over while the current
+// phase has the other one.
+struct RingPhase {
+    int uses;
+    unsigned parity;
+    uint64_t* clock;
+    bool over() const { return (unsigned)(uses & 1) != parity; }
+    bool poll() const {
+        *clock += moe::kPollNs;
+        return over();
+    }
+    uint64_t now() const { return *clock; }
+};
+
 }  // namespace
 
 extern "C" {
@@ -61,5 +76,20 @@ void wait_run(long long ends, long long other_gives_up, int later, long long* ou
     for (int i = 0; i < later; ++i) out[6] += moe::wait_bounded(Phase{&rest, -1, &gave_up, -1}, &gave_up) ? 1 : 0;
     out[4] = rest.t;
     out[5] = rest.polls;
+}
+
+// A ring of `size` entries of which the writer filled numbers 0 .. written - 1
+// and stopped: which of the entries 0 .. n - 1 a reader that takes one after the
+// other counts as written.
+void ring_run(int size, int written, int n, unsigned char* ok) {
+    volatile int gave_up = 0;
+    uint64_t clock = 0;
+    for (int j = 0; j < n; ++j) {
+        // what the entry's barrier shows a reader that is at number j: the
+        // writer is ahead of it by less than a round, or has stopped
+        int uses = 0;
+        for (int w = j % size; w < written && w <= j; w += size) ++uses;
+        ok[j] = moe::wait_written(RingPhase{uses, (unsigned)(j / size) & 1u, &clock}, &gave_up);
+    }
 }
 }
