@@ -227,8 +227,17 @@ class Pool:
 
     def plan_routed(self, logits, router, bias=None, rep_off=None, rep_ids=None, buf=0, stream=None):
         """moe_plan_routed: the plan with a scored router (a ``Router``);
-        ``bias`` fp32 [E] is added to the scores for the choice only."""
+        ``bias`` fp32 [E] is added to the scores for the choice only.  Every
+        tensor is contiguous and on the GPU: ``logits`` fp32 [T, E], ``rep_off``
+        int32 [E + 1], ``rep_ids`` int32 [P]; others are refused (ValueError)."""
         T = logits.shape[0]
+        _dense("logits", logits, torch.float32, (T, self.E))
+        if bias is not None:
+            _dense("bias", bias, torch.float32, (self.E,))
+        if rep_off is not None:
+            _dense("rep_off", rep_off, torch.int32, (self.E + 1,))
+        if rep_ids is not None:
+            _dense("rep_ids", rep_ids, torch.int32, (self.P,))
         _call("moe_plan_routed", self.handle, ctypes.byref(router), _ptr(logits), _ptr(bias), T, _ptr(rep_off),
               _ptr(rep_ids), buf, _stream(stream))
         return T
@@ -387,6 +396,18 @@ class Experts:
         """Wait for ``stream`` and return the device error word (0 = clean)."""
         (stream or torch.cuda.current_stream()).synchronize()
         return int(self.error_word.item())
+
+
+def _on_gpu(t):
+    return t.is_cuda
+
+
+def _dense(name, t, dtype, shape):
+    """A contiguous tensor of this type and shape on the GPU: what the library
+    reads from a bare pointer."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not _on_gpu(t):
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor {tuple(shape)} on the GPU, got "
+                         f"{'' if t.is_contiguous() else 'a strided '}{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _tensor(name, t, dtype, rows, width=None):

@@ -1,0 +1,73 @@
+"""The Python entry points of the expert layer refuse tensors that the library
+would misread or read past the end of: type, shape, strides and device.
+
+There is no GPU here: host tensors stand for device tensors (the device check is
+tested by itself), and a call past its checks can only report MOE_ERR_CUDA."""
+import ctypes
+
+import pytest
+import torch
+
+from combine_moe_plan_gb300 import build as moe_build
+from combine_moe_plan_gb300 import moe
+
+T, H, E, P, K = 8, 256, 16, 18, 4
+
+
+@pytest.fixture
+def pool(monkeypatch):
+    """A Pool over an address that nothing reads."""
+    moe_build.build()
+    p = moe.Pool.__new__(moe.Pool)
+    p.desc = moe.Desc(64, H, E, P, K, 128, 2)
+    p.T_max, p.H, p.E, p.P, p.k, p.n_sets = 64, H, E, P, K, 2
+    n, h = ctypes.c_size_t(), ctypes.c_void_p()
+    assert moe.lib().moe_pool_bytes(ctypes.byref(p.desc), ctypes.byref(n)) == 0
+    assert moe.lib().moe_pool_init(ctypes.byref(p.desc), ctypes.c_void_p(1 << 40), n, ctypes.byref(h)) == 0
+    p.handle, p._views = h, {}
+    monkeypatch.setattr(moe, "_stream", lambda stream: None)
+    return p
+
+
+@pytest.fixture
+def anywhere(monkeypatch):
+    monkeypatch.setattr(moe, "_on_gpu", lambda t: True)
+
+
+def strided(*shape, dtype=torch.float32):
+    """A view of this shape and type that skips every second element of a row."""
+    return torch.zeros(*shape[:-1], 2 * shape[-1], dtype=dtype)[..., ::2]
+
+
+def routed(pool, logits=None, bias=None, rep_off=None, rep_ids=None):
+    return pool.plan_routed(torch.zeros(T, E) if logits is None else logits, moe.Router(),
+                            torch.zeros(E) if bias is None else bias,
+                            torch.zeros(E + 1, dtype=torch.int32) if rep_off is None else rep_off,
+                            torch.zeros(P, dtype=torch.int32) if rep_ids is None else rep_ids)
+
+
+def test_plan_routed_takes_what_it_reads(pool, anywhere):
+    with pytest.raises(moe.MoeError) as e:
+        routed(pool)
+    assert e.value.rc == -6  # past every check
+    with pytest.raises(moe.MoeError) as e:
+        pool.plan_routed(torch.zeros(65, E), moe.Router())
+    assert e.value.rc == -2  # more tokens than the pool has
+
+
+@pytest.mark.parametrize("bad", [
+    dict(logits=torch.zeros(T, E, dtype=torch.bfloat16)), dict(logits=torch.zeros(T, E, dtype=torch.float64)),
+    dict(logits=torch.zeros(T, E - 1)), dict(logits=torch.zeros(T, E + 1)), dict(logits=torch.zeros(T * E)),
+    dict(logits=torch.zeros(E, T).t()), dict(logits=strided(T, E)), dict(bias=torch.zeros(E - 1)),
+    dict(bias=torch.zeros(E, dtype=torch.bfloat16)), dict(bias=strided(E)), dict(bias=torch.zeros(1, E)),
+    dict(rep_off=torch.zeros(E, dtype=torch.int32)), dict(rep_off=torch.zeros(E + 1, dtype=torch.int64)),
+    dict(rep_ids=torch.zeros(P - 1, dtype=torch.int32)), dict(rep_ids=torch.zeros(P, dtype=torch.int64)),
+    dict(rep_ids=strided(P, dtype=torch.int32))], ids=lambda b: next(iter(b)))
+def test_plan_routed_refuses(pool, anywhere, bad):
+    with pytest.raises(ValueError, match=next(iter(bad))):
+        routed(pool, **bad)
+
+
+def test_plan_routed_refuses_host_tensors(pool):
+    with pytest.raises(ValueError, match="on the GPU"):
+        routed(pool)
