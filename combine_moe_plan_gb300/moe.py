@@ -243,7 +243,9 @@ class Pool:
         return T
 
     def dispatch_f8(self, x, buf=0, stream=None):
-        """moe_dispatch_f8: dispatch with E4M3 codes (view()["codes_f8"])."""
+        """moe_dispatch_f8: dispatch with E4M3 codes (view()["codes_f8"]); ``x``
+        bf16 [T, H], contiguous, on the GPU."""
+        _dense("x", x, torch.bfloat16, (x.shape[0], self.H))
         _call("moe_dispatch_f8", self.handle, _ptr(x), x.shape[0], buf, _stream(stream))
 
     def experts(self, experts, T, h, h_scales, buf=0, stream=None):

@@ -71,3 +71,26 @@ def test_plan_routed_refuses(pool, anywhere, bad):
 def test_plan_routed_refuses_host_tensors(pool):
     with pytest.raises(ValueError, match="on the GPU"):
         routed(pool)
+
+
+def test_dispatch_f8_takes_what_it_reads(pool, anywhere):
+    with pytest.raises(moe.MoeError) as e:
+        pool.dispatch_f8(torch.zeros(T, H, dtype=torch.bfloat16))
+    assert e.value.rc == -9  # past every check of the tensor: nothing is planned
+    with pytest.raises(moe.MoeError) as e:
+        pool.dispatch_f8(torch.zeros(65, H, dtype=torch.bfloat16))
+    assert e.value.rc == -2
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(T, H), torch.zeros(T, H, dtype=torch.float16), torch.zeros(T, H - 128, dtype=torch.bfloat16),
+    torch.zeros(T, H + 128, dtype=torch.bfloat16), torch.zeros(T * H, dtype=torch.bfloat16),
+    torch.zeros(H, T, dtype=torch.bfloat16).t(), strided(T, H, dtype=torch.bfloat16)], ids=range(7))
+def test_dispatch_f8_refuses(pool, anywhere, bad):
+    with pytest.raises(ValueError, match="x: want"):
+        pool.dispatch_f8(bad)
+
+
+def test_dispatch_f8_refuses_host_tensors(pool):
+    with pytest.raises(ValueError, match="on the GPU"):
+        pool.dispatch_f8(torch.zeros(T, H, dtype=torch.bfloat16))
