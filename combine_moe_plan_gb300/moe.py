@@ -352,6 +352,7 @@ class Experts:
             _block_scaled("w13", w13, s13, P, 2 * I, H)
         if w2 is not None:
             _block_scaled("w2", w2, s2, P, H, I)
+        _all_on_gpu(*(t for t in (w13, s13, w2, s2) if t is not None))
         self.w13, self.s13, self.w2, self.s2 = w13, s13, w2, s2
         device = (w13 if w13 is not None else w2).device
         self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
@@ -375,6 +376,7 @@ class Experts:
         self._offsets(offsets)
         _tensor("h", h, torch.float8_e4m3fn, rows, self.I)
         h_stride = _tensor("h_scales", h_scales, torch.float32, rows)
+        _all_on_gpu(codes, scales, offsets, h, h_scales)
         _call("moe_experts_up", self._ref, codes.data_ptr(), scales.data_ptr(), stride, offsets.data_ptr(),
               rows, h.data_ptr(), h_scales.data_ptr(), h_stride, _stream(stream))
         return h, h_scales
@@ -386,6 +388,7 @@ class Experts:
         stride = _tensor("h_scales", h_scales, torch.float32, rows)
         self._offsets(offsets)
         _tensor("out", out, torch.bfloat16, rows, self.H)
+        _all_on_gpu(h, h_scales, offsets, out)
         _call("moe_experts_down", self._ref, h.data_ptr(), h_scales.data_ptr(), stride,
               offsets.data_ptr(), rows, out.data_ptr(), _stream(stream))
         return out
@@ -402,6 +405,12 @@ class Experts:
 
 def _on_gpu(t):
     return t.is_cuda
+
+
+def _all_on_gpu(*tensors):
+    for t in tensors:
+        if not _on_gpu(t):
+            raise ValueError(f"want every tensor on the GPU, got a {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _dense(name, t, dtype, shape):

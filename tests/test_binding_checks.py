@@ -94,3 +94,54 @@ def test_dispatch_f8_refuses(pool, anywhere, bad):
 def test_dispatch_f8_refuses_host_tensors(pool):
     with pytest.raises(ValueError, match="on the GPU"):
         pool.dispatch_f8(torch.zeros(T, H, dtype=torch.bfloat16))
+
+
+F8, INNER, ROWS = torch.float8_e4m3fn, 128, 6
+
+
+@pytest.fixture
+def experts(monkeypatch):
+    """Experts over addresses that nothing reads."""
+    moe_build.build()
+    e = moe.Experts.__new__(moe.Experts)
+    e.P, e.H, e.I = P, H, INNER
+    e.weights = moe.ExpertWeights(P, H, INNER, *[ctypes.c_void_p(1 << 41)] * 5)
+    e._ref = ctypes.byref(e.weights)
+    monkeypatch.setattr(moe, "_stream", lambda stream: None)
+    return e
+
+
+def products():
+    """Tensors of both products, by the name of their argument."""
+    offsets = torch.zeros(P + 1, dtype=torch.int32)
+    h, h_scales = torch.zeros(ROWS, INNER, dtype=F8), torch.zeros(ROWS, 4)
+    return {"up": dict(codes=torch.zeros(ROWS, H, dtype=F8), scales=torch.zeros(ROWS, 4), offsets=offsets, h=h,
+                       h_scales=h_scales),
+            "down": dict(h=h, h_scales=h_scales, offsets=offsets, out=torch.zeros(ROWS, H, dtype=torch.bfloat16))}
+
+
+HOST = [(call, name) for call, args in products().items() for name in args]
+
+
+@pytest.mark.parametrize("call,name", HOST)
+def test_experts_refuse_a_host_tensor(experts, monkeypatch, call, name):
+    args = products()[call]
+    monkeypatch.setattr(moe, "_on_gpu", lambda t: t is not args[name])
+    with pytest.raises(ValueError, match="on the GPU"):
+        getattr(experts, call)(**args)
+
+
+@pytest.mark.parametrize("call", ["up", "down"])
+def test_experts_take_device_tensors(experts, anywhere, call):
+    with pytest.raises(moe.MoeError) as e:
+        getattr(experts, call)(**products()[call])
+    assert e.value.rc == -6  # past every check
+
+
+@pytest.mark.parametrize("name", ["w13", "s13", "w2", "s2"])
+def test_experts_weights_on_the_host(monkeypatch, name):
+    w = dict(w13=torch.zeros(P, 2 * INNER, H, dtype=F8), s13=torch.zeros(P, 2 * INNER // 128, H // 128),
+             w2=torch.zeros(P, H, INNER, dtype=F8), s2=torch.zeros(P, H // 128, INNER // 128))
+    monkeypatch.setattr(moe, "_on_gpu", lambda t: t is not w[name])
+    with pytest.raises(ValueError, match="on the GPU"):
+        moe.Experts(**w)
