@@ -25,7 +25,9 @@ class ExpertLayer:
 
     ``E`` logical experts on the ``experts.P`` physical ones (``rep_off`` /
     ``rep_ids``: replica map, needed where P > E).  One call at a time per
-    buffer set; consecutive calls may alternate ``buf``."""
+    buffer set; consecutive calls may alternate ``buf``.  A call takes bf16
+    ``x`` [T, H], fp32 ``logits`` [T, E] and, if given, bf16 ``y`` [T, H], all
+    contiguous and on the GPU; others are refused (ValueError)."""
 
     def __init__(self, experts, T_max, E, k, router, bias=None, rep_off=None, rep_ids=None, n_sets=1):
         self.experts, self.router, self.bias = experts, router, bias
@@ -38,6 +40,10 @@ class ExpertLayer:
         if logits.shape[0] != T:
             raise ValueError("logits and x must have the same number of tokens")
         p = self.pool
+        # with these checked first (and the logits by the first call), an error leaves nothing enqueued
+        moe._dense("x", x, torch.bfloat16, (T, p.H))
+        if y is not None:
+            moe._dense("y", y, torch.bfloat16, (T, p.H))
         p.plan_routed(logits, self.router, self.bias, self.rep_off, self.rep_ids, buf=buf, stream=stream)
         p.dispatch_f8(x, buf=buf, stream=stream)
         p.experts(self.experts, T, *self.inner[buf], buf=buf, stream=stream)

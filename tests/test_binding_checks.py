@@ -145,3 +145,48 @@ def test_experts_weights_on_the_host(monkeypatch, name):
     monkeypatch.setattr(moe, "_on_gpu", lambda t: t is not w[name])
     with pytest.raises(ValueError, match="on the GPU"):
         moe.Experts(**w)
+
+
+class Recorder:
+    """A pool that notes its calls."""
+    H = H
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a, **k: self.calls.append(name)
+
+
+@pytest.fixture
+def net():
+    from combine_moe_plan_gb300 import layer
+    n = layer.ExpertLayer.__new__(layer.ExpertLayer)
+    n.pool, n.experts, n.router, n.bias, n.rep_off, n.rep_ids = Recorder(), None, moe.Router(), None, None, None
+    n.inner = [(None, None)]
+    return n
+
+
+BF = torch.bfloat16
+
+
+def test_expert_layer_calls_in_order(net, anywhere):
+    net(torch.zeros(T, H, dtype=BF), torch.zeros(T, E), torch.zeros(T, H, dtype=BF))
+    assert net.pool.calls == ["plan_routed", "dispatch_f8", "experts", "combine"]
+
+
+@pytest.mark.parametrize("x,y", [
+    (torch.zeros(T, H), None), (torch.zeros(T, H - 128, dtype=BF), None), (strided(T, H, dtype=BF), None),
+    (torch.zeros(T, H, dtype=BF), torch.zeros(T, H)), (torch.zeros(T, H, dtype=BF), torch.zeros(T - 1, H, dtype=BF)),
+    (torch.zeros(T, H, dtype=BF), torch.zeros(T, H - 128, dtype=BF)),
+    (torch.zeros(T, H, dtype=BF), strided(T, H, dtype=BF))], ids=range(7))
+def test_expert_layer_refuses_and_enqueues_nothing(net, anywhere, x, y):
+    with pytest.raises(ValueError, match="x: want" if y is None else "y: want"):
+        net(x, torch.zeros(T, E), y)
+    assert net.pool.calls == []
+
+
+def test_expert_layer_refuses_host_tensors(net):
+    with pytest.raises(ValueError, match="on the GPU"):
+        net(torch.zeros(T, H, dtype=BF), torch.zeros(T, E))
+    assert net.pool.calls == []
