@@ -282,11 +282,11 @@ int dispatch_call(moe_pool* pool, const uint16_t* x, int32_t T, int buf, bool x_
     if (T == 0) return MOE_OK;
     const moe_desc& d = pool->geo.d;
     const SetLayout& L = pool->geo.set[buf];
-    pool->e4m3[buf] = e4m3;
-    return cuda_rc(launch_dispatch(x, T, d.H, d.k, at<int32_t>(pool, L.slot), at<int8_t>(pool, L.codes),
-                                   at<float>(pool, L.scales), pool->geo.Gs,
-                                   at<int32_t>(pool, pool->geo.error_word), x_early, e4m3,
-                                   static_cast<cudaStream_t>(stream), &pool->launches));
+    rc = cuda_rc(launch_dispatch(x, T, d.H, d.k, at<int32_t>(pool, L.slot), at<int8_t>(pool, L.codes),
+                                 at<float>(pool, L.scales), pool->geo.Gs, at<int32_t>(pool, pool->geo.error_word),
+                                 x_early, e4m3, static_cast<cudaStream_t>(stream), &pool->launches));
+    if (rc == MOE_OK) pool->e4m3[buf] = e4m3;
+    return rc;
 }
 
 }  // namespace
@@ -322,8 +322,9 @@ MOE_API int moe_plan_dispatch(moe_pool* pool, const float* logits, int32_t T, co
 MOE_API int moe_identity_experts(moe_pool* pool, int32_t T, int buf, void* stream) {
     int rc = check_call(pool, T, buf);
     if (rc != MOE_OK) return rc;
-    if (pool->planned_T[buf] != T || pool->e4m3[buf]) return MOE_ERR_STATE;
+    if (pool->planned_T[buf] != T) return MOE_ERR_STATE;
     if (T == 0) return MOE_OK;
+    if (pool->e4m3[buf]) return MOE_ERR_STATE;
     const moe_desc& d = pool->geo.d;
     const SetLayout& L = pool->geo.set[buf];
     return cuda_rc(launch_identity_experts(at<int8_t>(pool, L.codes), at<float>(pool, L.scales), T * d.k, d.H,
