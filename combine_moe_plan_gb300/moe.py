@@ -18,7 +18,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
-MOE_OK = 0
+MOE_OK, MOE_ERR_STATE = 0, -9
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SIZE", -3: "MOE_ERR_ALIGN", -4: "MOE_ERR_BUF",
           -5: "MOE_ERR_WORKSPACE", -6: "MOE_ERR_CUDA", -7: "MOE_ERR_DEVICE", -8: "MOE_ERR_REPLICA",
           -9: "MOE_ERR_STATE"}
@@ -180,6 +180,7 @@ class Pool:
         _call("moe_pool_init", ctypes.byref(self.desc), _ptr(self.workspace), self.nbytes, ctypes.byref(h))
         self.handle = h
         self._views = {}
+        self._f8_tokens = [None] * n_sets  # tokens of each set's last dispatch, if that was in E4M3
         _call("moe_pool_clear_error", self.handle, _stream(stream))
 
     def __del__(self):
@@ -247,13 +248,18 @@ class Pool:
         bf16 [T, H], contiguous, on the GPU."""
         _dense("x", x, torch.bfloat16, (x.shape[0], self.H))
         _call("moe_dispatch_f8", self.handle, _ptr(x), x.shape[0], buf, _stream(stream))
+        self._f8_tokens[buf] = x.shape[0]
 
     def experts(self, experts, T, h, h_scales, buf=0, stream=None):
         """The set's rows (after ``dispatch_f8``) through ``experts``: their
         gated product into ``h`` / ``h_scales`` (``Experts.inner(rows)``), then
-        their down projection into the set's ex_out, ready for ``combine``."""
+        their down projection into the set's ex_out, ready for ``combine``.
+        Refused (MOE_ERR_STATE) unless the set's last dispatch was ``dispatch_f8``
+        with T tokens: INT8 rows would be read as E4M3."""
         if buf not in self._views:  # a set's buffers never move
             self._views[buf] = self.view(buf)
+        if self._f8_tokens[buf] != T:
+            raise MoeError("Pool.experts", MOE_ERR_STATE, lib().moe_status_str(MOE_ERR_STATE).decode())
         v, n = self._views[buf], T * self.k
         experts.up(v["codes_f8"], v["scales"], v["offsets"], h, h_scales, rows=n, stream=stream)
         experts.down(h, h_scales, v["offsets"], v["ex_out"], rows=n, stream=stream)
@@ -264,6 +270,7 @@ class Pool:
         this set's plan on the same stream, with x written before that plan."""
         fn = "moe_dispatch_after_plan" if after_plan else "moe_dispatch"
         _call(fn, self.handle, _ptr(x), x.shape[0], buf, _stream(stream))
+        self._f8_tokens[buf] = None
 
     def plan_dispatch(self, logits, x, rep_off=None, rep_ids=None, buf=0, stream=None):
         """moe_plan_dispatch: plan and dispatch as one call; the dispatch
@@ -273,6 +280,7 @@ class Pool:
             raise ValueError("logits and x must have the same number of tokens")
         _call("moe_plan_dispatch", self.handle, _ptr(logits), T, _ptr(rep_off), _ptr(rep_ids), _ptr(x), buf,
               _stream(stream))
+        self._f8_tokens[buf] = None
         return T
 
     def identity_experts(self, T, buf=0, stream=None):
@@ -288,6 +296,7 @@ class Pool:
         """Whole layer from host tensors (pinned for asynchronous copies)."""
         _call("moe_step_host", self.handle, _ptr(h_logits), _ptr(h_x), _ptr(h_ex_out), _ptr(h_y),
               h_x.shape[0], _ptr(rep_off), _ptr(rep_ids), buf, _stream(stream))
+        self._f8_tokens[buf] = None
 
     def clear_error(self, stream=None):
         _call("moe_pool_clear_error", self.handle, _stream(stream))

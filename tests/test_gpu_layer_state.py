@@ -42,3 +42,43 @@ def test_an_empty_int8_batch_after_an_e4m3_one():
         pool.identity_experts(5)
     assert e.value.rc == -9
     assert pool.check() == 0
+
+
+def weights(P, inner, seed=1):
+    from combine_moe_plan_gb300 import layer
+    return layer.random_experts(P, H, inner, seed=seed)
+
+
+def test_experts_want_the_set_dispatched_in_e4m3():
+    """Pool.experts reads E4M3 rows: refused for a set that holds INT8 rows, none
+    at all, or those of another number of tokens."""
+    pool = moe.Pool(16, H, E, E, K)
+    ex = weights(E, 128)
+    x, logits = inputs(6)
+    h, hs = ex.inner(12)
+
+    def refused(T=6, buf=0):
+        with pytest.raises(moe.MoeError) as e:
+            pool.experts(ex, T, h, hs, buf=buf)
+        assert e.value.rc == -9
+
+    refused()
+    for int8 in (lambda: pool.dispatch(x), lambda: pool.dispatch(x, after_plan=True),
+                 lambda: pool.plan_dispatch(logits, x),
+                 lambda: pool.step_host(logits.cpu().pin_memory(), x.cpu().pin_memory(),
+                                        torch.empty(6, H, dtype=torch.bfloat16).pin_memory())):
+        pool.plan(logits)
+        int8()
+        refused()
+        pool.plan(logits)
+        pool.dispatch_f8(x)
+        refused(T=5)
+        refused(buf=1)
+        pool.experts(ex, 6, h, hs)
+    with pytest.raises(moe.MoeError) as e:
+        pool.experts(ex, 6, h, hs, buf=2)
+    assert e.value.rc == -4
+    pool.plan(logits[:0])
+    pool.dispatch_f8(x[:0])
+    pool.experts(ex, 0, h, hs)
+    assert pool.check() == 0 and ex.check() == 0
