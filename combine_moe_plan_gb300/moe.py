@@ -371,10 +371,11 @@ class Experts:
 
     def inner(self, rows):
         """Buffers for ``rows`` rows between the two products: E4M3 [rows, I]
-        and fp32 scales [rows, I / 128 rounded up to 4]."""
+        and fp32 scales [rows, I / 128 rounded up to 4], neither filled: a fill
+        would be of the current stream, and could run after a product of another."""
         dev = self.error_word.device
         return (torch.empty((rows, self.I), dtype=torch.float8_e4m3fn, device=dev),
-                torch.zeros((rows, (self.I // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
+                torch.empty((rows, (self.I // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
 
     def up(self, codes, scales, offsets, h, h_scales, rows=None, stream=None):
         """h, h_scales = quantised silu(rows gate^T) * (rows up^T) per window;

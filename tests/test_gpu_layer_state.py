@@ -82,3 +82,28 @@ def test_experts_want_the_set_dispatched_in_e4m3():
     pool.dispatch_f8(x[:0])
     pool.experts(ex, 0, h, hs)
     assert pool.check() == 0 and ex.check() == 0
+
+
+def busy(ms=100):
+    """Keep the current stream busy for about so long."""
+    torch.cuda._sleep(int(ms * 2e6))
+
+
+def test_buffers_made_on_a_busy_stream():
+    """Experts.inner leaves nothing behind on the stream it is called on that
+    could run after a product on another one."""
+    ex = weights(1, 256)
+    n = 40
+    rows = (torch.randn(n, H, generator=gen(2), device="cuda") * 40).to(torch.float8_e4m3fn)
+    scales = torch.full((n, 4), 0.02, device="cuda")
+    offsets = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    want = [t.clone() for t in ex.up(rows, scales, offsets, *ex.inner(n))]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    busy()
+    h, hs = ex.inner(n)
+    ex.up(rows, scales, offsets, h, hs, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(hs[:, :2], want[1][:, :2]) and bool((hs[:, :2] > 0).any())
+    assert torch.equal(h.view(torch.uint8), want[0].view(torch.uint8))
+    assert ex.check() == 0
