@@ -34,6 +34,8 @@ class ExpertLayer:
         self.rep_off, self.rep_ids = rep_off, rep_ids
         self.pool = moe.Pool(T_max, experts.H, E, experts.P, k, n_sets=n_sets)
         self.inner = [experts.inner(T_max * k) for _ in range(n_sets)]
+        # the pool's error word is zeroed on this stream: before another stream's call may set it
+        torch.cuda.current_stream(experts.error_word.device).synchronize()
 
     def __call__(self, x, logits, y=None, buf=0, stream=None):
         T = x.shape[0]

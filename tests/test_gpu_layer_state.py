@@ -107,3 +107,25 @@ def test_buffers_made_on_a_busy_stream():
     assert torch.equal(hs[:, :2], want[1][:, :2]) and bool((hs[:, :2] > 0).any())
     assert torch.equal(h.view(torch.uint8), want[0].view(torch.uint8))
     assert ex.check() == 0
+
+
+def test_a_layer_made_on_a_busy_stream():
+    """An error bit that a call on another stream sets is not wiped by the
+    layer's construction."""
+    from combine_moe_plan_gb300 import layer
+    ex = weights(E, 128)
+    x, logits = inputs(6)
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda")
+    ids = torch.arange(E, dtype=torch.int32, device="cuda")
+    ids[:] = E  # no such expert: every copy is skipped and reported
+    y = torch.zeros_like(x)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # the kernels are loaded by a first layer, and its memory is the next one's: nothing below waits for the GPU
+    layer.ExpertLayer(ex, 16, E, K, moe.Router(), rep_off=off, rep_ids=ids)(x, logits, y, stream=other)
+    torch.cuda.synchronize()
+    busy()
+    net = layer.ExpertLayer(ex, 16, E, K, moe.Router(), rep_off=off, rep_ids=ids)
+    net(x, logits, y, stream=other)
+    torch.cuda.synchronize()
+    assert net.check() & moe.DEVERR_REPLICA
