@@ -151,11 +151,11 @@ struct TopkSoftmax {
 //   largest choices; the topk_group best groups stay (equal scores: the lower
 //   group); the k largest choices in them are taken (equal: the lower id);
 //   gate = s_e, over the sum of the k selected scores if renorm, times scale.
-// The softmax's sum is carried as a pair of floats, so it does not depend on
-// the order of its terms: the choices, and with them every integer the plan
-// writes, are functions of the inputs alone, whatever the lanes per token.
-// (64-bit fixed point would do as well; its conversions cost 0.4 us more a plan
-// of 96 tokens.)
+// The softmax's sum is that of its terms rounded to multiples of 2^-41
+// (GridSum), which is exact in any order: the choices, and with them every
+// integer the plan writes, are functions of the inputs alone, whatever the lanes
+// per token.  (64-bit fixed point would do as well; its conversions cost 0.4 us
+// more a plan of 96 tokens.)
 struct ScoreRouter {
     static constexpr bool kScored = true;
     const float* bias;  // [E] or NULL
@@ -273,6 +273,37 @@ __device__ __forceinline__ void load_run(const float* __restrict__ src, int n, i
     }
 }
 
+// A sum of up to 1024 terms in [0, 1] that does not depend on their order: each
+// term is cut into multiples of 2^-13, 2^-27 and 2^-41 (what is left, at most
+// 2^-42, is dropped), and each kind is summed by itself.  A sum of one kind is a
+// multiple of its grid and below 2^24 of it, so every addition is exact.  Adding
+// and taking away 1.5 x 2^(23 - g) rounds to a multiple of 2^-g (Rump, Ogita and
+// Oishi, "Accurate floating-point summation", SIAM J. Sci. Comput. 31(1), 2008).
+struct GridSum {
+    float hi = 0.0f, mid = 0.0f, lo = 0.0f;
+    static __device__ __forceinline__ float cut(float& v, float c) {
+        const float q = __fsub_rn(__fadd_rn(v, c), c);
+        v = __fsub_rn(v, q);
+        return q;
+    }
+    __device__ __forceinline__ void add(float e) {
+        hi = __fadd_rn(hi, cut(e, 0x1.8p10f));
+        mid = __fadd_rn(mid, cut(e, 0x1.8p-4f));
+        lo = __fadd_rn(lo, cut(e, 0x1.8p-18f));
+    }
+    __device__ __forceinline__ void add_lane(int off) {  // the sum of lane ^ off
+        hi = __fadd_rn(hi, __shfl_xor_sync(kFull, hi, off));
+        mid = __fadd_rn(mid, __shfl_xor_sync(kFull, mid, off));
+        lo = __fadd_rn(lo, __shfl_xor_sync(kFull, lo, off));
+    }
+    // to the nearest binary32, but for sums within 2^-47 of the middle of two
+    __device__ __forceinline__ float value() const {
+        const dword::dw t = dword::two_sum(mid, lo);
+        const dword::dw u = dword::two_sum(hi, t.h);
+        return __fadd_rn(u.h, __fadd_rn(u.l, t.l));
+    }
+};
+
 // The keys of a scored router: the order keys of the choices of experts
 // [e0, e0 + st) of one token (0 past E and for a token past T), groups
 // applied.  A segment of L lanes holds a token; every lane of the warp takes
@@ -294,18 +325,15 @@ __device__ __forceinline__ void scored_keys(const ScoreRouter& ro, const float* 
         for (int r = 1; r < EPL; ++r) m = fmaxf(m, v[r]);
 #pragma unroll
         for (int off = 1; off < L; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-        dword::dw sum = {0.0f, 0.0f};
+        GridSum sum;
 #pragma unroll
         for (int r = 0; r < EPL; ++r) {
-            float e = expf(v[r] - m);  // 0 past E
-            if (!(e == e)) e = 0.0f;   // a NaN logit, or no finite one
-            const dword::dw t = dword::two_sum(sum.h, e);
-            sum = dword::fast_two_sum(t.h, sum.l + t.l);
+            const float e = expf(v[r] - m);  // 0 past E
+            sum.add(e == e ? e : 0.0f);      // NaN: a NaN logit, or no finite one
         }
 #pragma unroll
-        for (int off = 1; off < L; off <<= 1)
-            sum = dword::dw_add(sum, dword::dw{__shfl_xor_sync(kFull, sum.h, off), __shfl_xor_sync(kFull, sum.l, off)});
-        ms = make_float2(m, sum.h);
+        for (int off = 1; off < L; off <<= 1) sum.add_lane(off);
+        ms = make_float2(m, sum.value());
     }
     if (sl == 0) *stat = ms;
 #pragma unroll
