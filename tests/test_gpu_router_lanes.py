@@ -1,8 +1,14 @@
-"""moe_plan_routed with every number of lanes a token: the same bits.
+"""moe_plan_routed with every number of lanes a token: the same bits, and right
+against the plain implementation in 64 bits; and without clusters.
 
 Lanes: a warp a token in a cluster or ticket plan, in three launches with groups,
 more than 64 experts, or 17 to 64 up to 4864 tokens; else 8 (k up to 8) or 16.
 """
+import os
+import re
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -10,7 +16,9 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from tests.gpu_util import ensure_built  # noqa: E402
-from tests.test_gpu_router import run  # noqa: E402
+from tests.test_gpu_router import check, grid_logits, run  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -77,3 +85,51 @@ def test_few_experts_do_not_depend_on_the_lanes(E, k):
     rng = np.random.default_rng([E, k])
     logits = (rng.standard_normal((700, E)) * 6).astype(np.float32)
     same_alone(logits, logits, (rng.integers(-20, 20, E) / 1000).astype(np.float32), k, [(0, 512), (512, 700), (9, 10)])
+
+
+def clear(logits, bias, score, k):
+    """Replace rows in which two choices around the first k + 1 are closer than
+    their rounding (but not equal: equal logits and biases are ties by
+    definition) by the first row without any."""
+    x = logits.astype(np.float64)
+    if score == "sigmoid":
+        s = 1.0 / (1.0 + np.exp(-x))
+    else:
+        e = np.exp(x - x.max(1, keepdims=True))
+        s = e / e.sum(1, keepdims=True)
+    c = -np.sort(-(s if bias is None else s + bias), axis=1)[:, :k + 2]
+    gap = c[:, :-1] - c[:, 1:]
+    # a score is off by less than 2^-20 of itself (its argument spans 8 units); a sum is rounded to 2^-24
+    near = ((gap < 2.0 ** -19 * np.abs(c[:, :-1])) & (gap > 0)).any(1)
+    if bias is not None:
+        near |= (gap == 0).any(1)
+    assert not near.all()
+    logits[near] = logits[np.argmin(near)]
+    return logits
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,T", [(16, 12, 513), (16, 9, 2100), (9, 9, 600), (64, 12, 4865), (40, 16, 5000),
+                                   (64, 5, 4865), (17, 8, 4865), (16, 8, 513)])
+def test_eight_and_sixteen_lanes(E, k, T, score):
+    rng = np.random.default_rng([E, k, T])
+    logits = grid_logits(rng, T, E)
+    bias = (rng.integers(-50, 50, E) / 1000).astype(np.float32)
+    check(clear(logits.copy(), None, score, k), None, k, score=score, scale=2.0)
+    check(clear(logits.copy(), bias, score, k), bias, k, score=score, renorm=False)
+
+
+# test_gpu_router's cases without groups, by name, that pass the limits of the
+# ticket plan (4 tiles of 32 tokens) and of the three launches' small tiles.
+NAMES = [f"test_batch_sizes_without_groups[{E}-{k}-{T}]"
+         for E, k in ((8, 2), (64, 6), (128, 16), (256, 8), (600, 32), (1, 1)) for T in (1, 64, 128, 129, 512, 513, 2049)]
+
+
+def test_every_batch_size_without_clusters():
+    if os.environ.get("MOE_PLAN_NO_CLUSTER") == "1":
+        pytest.skip("already without clusters")
+    path = os.path.join(ROOT, "tests", "test_gpu_router.py")
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-m", "gpu", *[f"{path}::{n}" for n in NAMES]],
+                       env=dict(os.environ, MOE_PLAN_NO_CLUSTER="1"), capture_output=True, text=True, timeout=600, cwd=ROOT)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
+    assert re.search(rf"\b{len(NAMES)} passed", r.stdout), r.stdout[-500:]
