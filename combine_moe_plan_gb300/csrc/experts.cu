@@ -238,12 +238,15 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                const Problem pr) {
     constexpr int kStages = Layout<UP>::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
-    const uint32_t skip = (1024u - (smem_u32(smem) & 1023u)) % 1024u;  // 0 unless the base moved
+    const uint32_t skip = (1024u - (smem_u32(smem) & 1023u)) % 1024u;
     unsigned char* stages = smem + skip;
     unsigned char* staged = stages + kStages * kStageBytes;
     Barriers& b = *reinterpret_cast<Barriers*>(stages + Layout<UP>::kBytes);
-    // Room is reserved for an aligned base; another one is refused, not run over.
+    // The kernel has no other shared memory, so the base lies on a 1024-byte
+    // boundary.  One that does not is refused, for there is no room to skip to
+    // the next boundary.
     if (skip + Layout<UP>::kBytes + sizeof(Barriers) + (pr.P + 1) * sizeof(int) > dynamic_smem_bytes()) {
+        grid_dependency_sync();  // no kernel behind this one starts before those in front of it are done
         if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
         return;
     }

@@ -90,7 +90,8 @@ typedef enum moe_status {
 #define MOE_DEVERR_DUPLICATE 0x2 /* a token mapped twice to one physical expert */
 #define MOE_DEVERR_SLOT 0x4      /* a slot index outside [0, T*k) */
 #define MOE_DEVERR_WINDOW 0x8    /* an expert window outside the rows (moe_experts_*) */
-#define MOE_DEVERR_STALL 0x10    /* a wait inside moe_experts_* ran out */
+#define MOE_DEVERR_STALL 0x10    /* moe_experts_* gave up: a wait inside it ran out (its outputs are
+                                    void), or its shared memory is not as it expects (nothing done) */
 
 /*
  * Pool geometry, fixed at init (static pre-allocation: write-up,
