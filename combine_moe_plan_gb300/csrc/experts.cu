@@ -25,13 +25,16 @@
 // GB): 927 us, 6.9 TB/s, 1.02 of the measured copy peak.  4096 tokens, 288
 // experts (8.8 GB): 1.31 ms from a cool GPU (0.98), 1.41 to 1.47 ms at its power
 // limit, where the SM clock falls to 1.5 GHz.  Many rows: 98,304 rows over 64
-// experts of 2048 x 1024, first product 316 us cool (2.6 PFLOP/s, 1.35 of the
-// measured bf16 burst), 366 at the power limit; second 191 and 212.  There a
-// block takes about 790 cycles, of which the product alone needs 543 (alone on
-// the SM; the tensor pipe counts 42 % active) and the multiply-adds 256 of the
-// FMA pipe: the summing warps' own time, wait + read and add (420) + release +
-// loop, is what is left, and reading TMEM is not (loads of 16 columns cost 21
-// cycles one by one and do not slow the product).
+// experts of 2048 x 1024, first product 330 us cool (2.5 PFLOP/s, 1.30 of the
+// measured bf16 burst), 371 at the power limit; second 196 and 213.  There a
+// block takes about 790 cycles, which no unit fills: the product needs 543 (alone
+// on the SM; the tensor pipe counts 42 % active), the multiply-adds 256 of the
+// FMA pipe, and reading and adding a block up takes a summing warp 420.  Taking
+// the sums away shortens the first product to 214 us, so they are on the critical
+// path; the other 370 cycles of a block, and about 2500 that a change of tile
+// takes (the end of a tile runs in the summing warps, between two summing loops),
+// have not been traced.  Reading TMEM is not what bounds it (loads of 16 columns
+// cost 21 cycles one by one and do not slow the product).
 //
 // Measured and left out: 16 summing warps (434 against 402 us at the time);
 // accumulators of 128 columns with two issuing threads (419 / 357); 32 or 64

@@ -168,9 +168,10 @@ struct ScoreRouter {
     // Above 64 experts its rounds, with a ballot in place of a second
     // reduction, are the shorter ones (4096 tokens, 128 experts, top-8: 9.5 us
     // against 19.3 with 16 lanes); from 17 to 64 as long as every tile has an SM
-    // to itself (64 experts, top-6: 2048 tokens 7.8 us against 8.8 with 8 lanes,
-    // 4096 8.0 / 9.1, but 12288 13.7 / 12.1, 16384 16.6 / 14.1); below that 8
-    // lanes do (16384 tokens, 16 experts: 7.9 against 12.4).
+    // to itself (softmax, top-6, 4096 tokens: 64 experts 7.8 us against 9.2 with 8
+    // lanes, 32 experts 7.0 / 7.6, 20 experts 7.0 / 7.4; but 8192 tokens of 20
+    // experts 8.6 / 8.0, 16384 of 64 16.6 / 14.1); up to 16 experts 8 lanes do
+    // (4096 tokens 7.0 with a warp / 6.6, 16384 tokens 12.4 / 7.9).
     bool whole_warps(int T, int E) const {
         constexpr int kTilePerSm = 152 * kTileTokens;  // tokens
         return n_group > 1 || E > 64 || (E > 16 && T <= kTilePerSm);

@@ -254,7 +254,9 @@ typedef struct moe_router {
  * the same kernels and forms, and the same arguments and errors; a router
  * outside the ranges above is MOE_ERR_SIZE.  A logit of -inf has score 0, and
  * so has a NaN; a token whose logits are all -inf takes the lowest ids of the
- * first groups with gates 0 (softmax).  A bias of -inf keeps an expert from
+ * first groups with gates 0 (softmax).  So does, with softmax scores and without
+ * a bias, a token with a logit of +inf, for which all its scores are 0; a
+ * sigmoid's score of +inf is 1.  A bias of -inf keeps an expert from
  * being chosen while the allowed groups hold k others.
  */
 MOE_API int moe_plan_routed(moe_pool* pool, const moe_router* router, const float* logits, const float* bias,
@@ -376,7 +378,10 @@ MOE_API int moe_experts_down(const moe_experts* experts, const uint8_t* h, const
 /*
  * Identity experts (test stand-in for the expert FFNs): for rows r < T*k,
  * ex_out[r, i] = bf16(codes[r, i] * scales[r, i/128]).  Requires a prior
- * moe_plan and moe_dispatch on this set with the same T.
+ * moe_plan and moe_dispatch on this set with the same T (MOE_ERR_STATE for another
+ * T, or if the set was last dispatched by moe_dispatch_f8; T = 0: no-op).  T and
+ * the type of the codes are those of the last calls made on the set, captured
+ * ones included: replaying a graph does not change them.
  */
 MOE_API int moe_identity_experts(moe_pool* pool, int32_t T, int buf, void* stream);
 

@@ -119,6 +119,26 @@ def test_eight_and_sixteen_lanes(E, k, T, score):
     check(clear(logits.copy(), bias, score, k), bias, k, score=score, renorm=False)
 
 
+@pytest.mark.parametrize("T", [5, 600, 5000])
+def test_logits_of_plus_infinity(T):
+    """As include/moe.h says: every softmax score of such a token is 0 (its gates
+    are 0, its ids the lowest); a sigmoid's score is 1.  The others are untouched."""
+    rng = np.random.default_rng(T)
+    logits = grid_logits(rng, T, 64)
+    bad = logits.copy()
+    bad[3, 40] = np.inf
+    rest = np.r_[0:3, 4:T]
+    for renorm in (False, True):
+        a = run(logits, None, 4, score="softmax", renorm=renorm)
+        b = run(bad, None, 4, score="softmax", renorm=renorm)
+        np.testing.assert_array_equal(b["topk_e"][3], np.arange(4))
+        np.testing.assert_array_equal(b["gates"][3], 0)
+        np.testing.assert_array_equal(b["topk_e"][rest], a["topk_e"][rest])
+        np.testing.assert_array_equal(b["gates"][rest], a["gates"][rest])
+    b = run(bad, None, 4, score="sigmoid", renorm=False)
+    assert b["topk_e"][3][0] == 40 and b["gates"][3][0] == 1.0
+
+
 # test_gpu_router's cases without groups, by name, that pass the limits of the
 # ticket plan (4 tiles of 32 tokens) and of the three launches' small tiles.
 NAMES = [f"test_batch_sizes_without_groups[{E}-{k}-{T}]"
