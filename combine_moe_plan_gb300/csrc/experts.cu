@@ -367,13 +367,13 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
             }
-            if (!ok) {  // leave only after the copies in flight have landed (or not at all)
-                set_error(pr.err, MOE_DEVERR_STALL);
-                const uint64_t t0 = now_ns();
-                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    while (!mbar_try(smem_u32(&b.full[i % kStages]), (i / kStages) & 1) && now_ns() - t0 < kStallNs) {
-                    }
-            }
+            if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
+            // Leave only after the copies in flight have landed (or never will),
+            // also where this thread was through before another wait gave up.
+            const uint64_t t0 = now_ns();
+            for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                while (!mbar_try(smem_u32(&b.full[i % kStages]), (i / kStages) & 1) && now_ns() - t0 < kStallNs) {
+                }
         }
         if (warp == kMmaWarp && elect_one()) {
             int s = 0;
@@ -408,12 +408,10 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
             }
-            if (!ok) {
-                set_error(pr.err, MOE_DEVERR_STALL);
-                umma_commit(&b.drain);
-                const uint64_t t0 = now_ns();
-                while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
-                }
+            if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
+            umma_commit(&b.drain);  // the same for the products in flight
+            const uint64_t t0 = now_ns();
+            while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
             }
         }
         if (warp >= kStoreWarp) {
