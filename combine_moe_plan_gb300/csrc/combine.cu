@@ -27,7 +27,9 @@ constexpr int kCombineThreads = 256;  // 8 warps
 constexpr int kChunks = 1;            // 16-byte chunks per lane per item
 constexpr int kSegElems = 32 * 8 * kChunks;
 
-template <int KB>  // copies loaded before accumulating
+// KB: copies loaded before accumulating.  GATED: weighted by the gates
+// (moe_combine), or the plain sum (moe_gather).
+template <int KB, bool GATED>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(const uint16_t* __restrict__ ex_out, const int32_t* __restrict__ slot,
                const float* __restrict__ gates, int T, int H, int k, uint16_t* __restrict__ y,
@@ -53,7 +55,7 @@ combine_kernel(const uint16_t* __restrict__ ex_out, const int32_t* __restrict__ 
     float my_gate = 0.0f;
     if (lane < k) {
         my_slot = slot[(size_t)t * k + lane];
-        my_gate = gates[(size_t)t * k + lane];
+        my_gate = GATED ? gates[(size_t)t * k + lane] : 1.0f;
     }
     int bad = (lane < k) && (my_slot < 0 || my_slot >= rows);
     bad = __any_sync(kFull, bad);
@@ -136,8 +138,8 @@ cudaError_t launch_combine(const uint16_t* ex_out, const int32_t* slot, const fl
     const long long blocks = (items + (kCombineThreads / 32) - 1) / (kCombineThreads / 32);
     cudaError_t e;
 #define MOE_COMBINE_CASE(KB)                                                                                    \
-    e = launch_pdl(combine_kernel<KB>, dim3((unsigned)blocks), dim3(kCombineThreads), 0, s, ex_out, slot, gates, \
-                   T, H, k, y, err)
+    e = launch_pdl(gates != nullptr ? combine_kernel<KB, true> : combine_kernel<KB, false>,                      \
+                   dim3((unsigned)blocks), dim3(kCombineThreads), 0, s, ex_out, slot, gates, T, H, k, y, err)
     switch (k < 8 ? k : 8) {
         case 1: MOE_COMBINE_CASE(1); break;
         case 2: MOE_COMBINE_CASE(2); break;

@@ -172,9 +172,19 @@ cudaError_t launch_dispatch(const uint16_t* x, int T, int H, int k, const int32_
 cudaError_t launch_identity_experts(const int8_t* codes, const float* scales, int rows, int H, int Gs,
                                     uint16_t* ex_out, cudaStream_t s, uint64_t* launches);
 
+// gates NULL: the plain sum of the rows (moe_gather).
 cudaError_t launch_combine(const uint16_t* ex_out, const int32_t* slot, const float* gates,
                            int T, int H, int k, uint16_t* y, int32_t* err,
                            cudaStream_t s, uint64_t* launches);
+
+cudaError_t launch_scatter(const uint16_t* x, int T, int H, int k, const int32_t* slot, const float* gates,
+                           uint16_t* rows, float* row_gates, int32_t* err, cudaStream_t s, uint64_t* launches);
+
+// router, logits NULL: moe_plan's gates.
+cudaError_t launch_gates_backward(const moe_router* router, const float* logits, const float* gates,
+                                  const int32_t* topk_e, const int32_t* slot, const float* gate_parts, int parts,
+                                  int T, int E, int k, float* dgates, float* dlogits, int32_t* err, cudaStream_t s,
+                                  uint64_t* launches);
 
 }  // namespace moe
 
@@ -183,5 +193,6 @@ struct moe_pool {
     char* base;                       // device workspace
     int32_t planned_T[moe::kMaxSets]; // T of the last moe_plan per set (-1 = none)
     bool e4m3[moe::kMaxSets];         // the set's codes were last written by moe_dispatch_f8
+    bool routed[moe::kMaxSets];       // the set was last planned by moe_plan_routed
     uint64_t launches;
 };

@@ -157,6 +157,7 @@ int plan_call(moe_pool* pool, const moe_router* router, const float* logits, con
                            &pool->launches);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     pool->planned_T[buf] = T;
+    pool->routed[buf] = router != nullptr;
     return MOE_OK;
 }
 
@@ -347,6 +348,56 @@ MOE_API int moe_combine(moe_pool* pool, const uint16_t* ex_out, uint16_t* y, int
                                   &pool->launches));
 }
 
+MOE_API int moe_scatter(moe_pool* pool, const uint16_t* x, int32_t T, uint16_t* rows, float* row_gates, int buf,
+                        void* stream) {
+    int rc = check_call(pool, T, buf);
+    if (rc != MOE_OK) return rc;
+    if (T > 0 && (x == nullptr || rows == nullptr)) return MOE_ERR_NULL;
+    if (T > 0 && (!aligned16(x) || !aligned16(rows) || !aligned16(row_gates))) return MOE_ERR_ALIGN;
+    if (pool->planned_T[buf] != T) return MOE_ERR_STATE;
+    if (T == 0) return MOE_OK;
+    const moe_desc& d = pool->geo.d;
+    const SetLayout& L = pool->geo.set[buf];
+    return cuda_rc(launch_scatter(x, T, d.H, d.k, at<int32_t>(pool, L.slot), at<float>(pool, L.gates), rows, row_gates,
+                                  at<int32_t>(pool, pool->geo.error_word), static_cast<cudaStream_t>(stream),
+                                  &pool->launches));
+}
+
+MOE_API int moe_gather(moe_pool* pool, const uint16_t* rows, uint16_t* y, int32_t T, int buf, void* stream) {
+    int rc = check_call(pool, T, buf);
+    if (rc != MOE_OK) return rc;
+    if (T > 0 && (rows == nullptr || y == nullptr)) return MOE_ERR_NULL;
+    if (T > 0 && (!aligned16(rows) || !aligned16(y))) return MOE_ERR_ALIGN;
+    if (pool->planned_T[buf] != T) return MOE_ERR_STATE;
+    if (T == 0) return MOE_OK;
+    const moe_desc& d = pool->geo.d;
+    const SetLayout& L = pool->geo.set[buf];
+    return cuda_rc(launch_combine(rows, at<int32_t>(pool, L.slot), nullptr, T, d.H, d.k, y,
+                                  at<int32_t>(pool, pool->geo.error_word), static_cast<cudaStream_t>(stream),
+                                  &pool->launches));
+}
+
+MOE_API int moe_gates_backward(moe_pool* pool, const moe_router* router, const float* logits, const float* gate_parts,
+                               int32_t parts, int32_t T, float* dgates, float* dlogits, int buf, void* stream) {
+    int rc = check_call(pool, T, buf);
+    if (rc != MOE_OK) return rc;
+    if (parts < 1 || parts > 512) return MOE_ERR_SIZE;
+    if (T > 0 && (router == nullptr) != (logits == nullptr)) return MOE_ERR_NULL;
+    if (T > 0 && (gate_parts == nullptr || dgates == nullptr || dlogits == nullptr)) return MOE_ERR_NULL;
+    if (router != nullptr && (rc = check_router(pool->geo.d, *router)) != MOE_OK) return rc;
+    if (T > 0 && (!aligned16(logits) || !aligned16(gate_parts) || !aligned16(dgates) || !aligned16(dlogits)))
+        return MOE_ERR_ALIGN;
+    if (pool->planned_T[buf] != T) return MOE_ERR_STATE;
+    if (T == 0) return MOE_OK;
+    if (pool->routed[buf] != (router != nullptr)) return MOE_ERR_STATE;
+    const moe_desc& d = pool->geo.d;
+    const SetLayout& L = pool->geo.set[buf];
+    return cuda_rc(launch_gates_backward(router, logits, at<float>(pool, L.gates), at<int32_t>(pool, L.topk_e),
+                                         at<int32_t>(pool, L.slot), gate_parts, parts, T, d.E, d.k, dgates, dlogits,
+                                         at<int32_t>(pool, pool->geo.error_word), static_cast<cudaStream_t>(stream),
+                                         &pool->launches));
+}
+
 MOE_API int moe_step_host(moe_pool* pool, const float* h_logits, const uint16_t* h_x, const uint16_t* h_ex_out,
                           uint16_t* h_y, int32_t T, const int32_t* rep_off, const int32_t* rep_ids, int buf,
                           void* stream) {
@@ -391,7 +442,7 @@ MOE_API const char* moe_status_str(int status) {
         case MOE_ERR_CUDA: return "CUDA runtime call failed";
         case MOE_ERR_DEVICE: return "kernel reported a bad index (device error word)";
         case MOE_ERR_REPLICA: return "malformed replica map";
-        case MOE_ERR_STATE: return "T differs from the T planned for this buffer set, or its codes are of another type";
+        case MOE_ERR_STATE: return "T differs from the T planned for this buffer set, or its codes or plan are of another kind";
         default: return "unknown status";
     }
 }

@@ -56,6 +56,98 @@ class ExpertLayer:
         return self.pool.check() | self.experts.check()
 
 
+class TrainingLayer:
+    """The same layer in bf16 with gradients: scored (``router``) or top-k softmax
+    routing, bf16 rows, the experts' products, combine; and back.
+
+    ``forward`` keeps, per buffer set, x (by reference: leave it alone until the
+    set's ``backward``), the plan, and the experts' gate and up values in 8 bits;
+    rows and experts' outputs are not kept.  ``backward`` takes the gradient of y
+    and returns those of x and the logits; the weights' gradients go to ``dw13``
+    and ``dw2`` (fp32, added up with ``accumulate``; or bf16).  A replica's weights
+    have a gradient of their own.  Several sets may be forward before the first
+    goes backward (gradient accumulation, pipelining); the buffers of rows are
+    shared, so all calls go to one stream, or wait for one another."""
+
+    def __init__(self, w13, w2, T_max, E, k, router=None, bias=None, rep_off=None, rep_ids=None, n_sets=1):
+        if router is None and bias is not None:
+            raise ValueError("a bias needs a router")
+        self.experts = ex = moe.DenseExperts(w13, w2)
+        self.router, self.bias, self.rep_off, self.rep_ids = router, bias, rep_off, rep_ids
+        self.pool = moe.Pool(T_max, ex.H, E, ex.P, k, n_sets=n_sets)
+        self.views = [self.pool.view(b) for b in range(n_sets)]
+        n, dev = T_max * k, ex.error_word.device
+        self.kept = [ex.kept(n) for _ in range(n_sets)]
+        self.saved = [None] * n_sets
+
+        def rows(width, dtype=torch.bfloat16):
+            return torch.empty((n, width), dtype=dtype, device=dev)
+
+        self.x_rows, self.d_rows = rows(ex.H), rows(ex.H)  # tokens in their windows; their gradients
+        self.h, self.dgu = rows(ex.I), rows(2 * ex.I)
+        self.parts = rows(ex.I // 128, torch.float32)
+        self.row_gates = torch.empty(n, device=dev)
+        # the pool's error word is zeroed on this stream: before another stream's call may set it
+        torch.cuda.current_stream(dev).synchronize()
+
+    def forward(self, x, logits, y=None, buf=0, stream=None):
+        T, p, ex = x.shape[0], self.pool, self.experts
+        if not 0 <= buf < len(self.saved):
+            raise ValueError(f"buf: want one of {len(self.saved)} sets, got {buf}")
+        # with these checked first, an error leaves nothing enqueued
+        moe._dense("x", x, torch.bfloat16, (T, p.H))
+        moe._dense("logits", logits, torch.float32, (T, p.E))
+        if T > p.T_max:
+            raise ValueError(f"x: at most {p.T_max} tokens, got {T}")
+        if y is not None:
+            moe._dense("y", y, torch.bfloat16, (T, p.H))
+        self.saved[buf] = None
+        if self.router is None:
+            p.plan(logits, self.rep_off, self.rep_ids, buf=buf, stream=stream)
+        else:
+            p.plan_routed(logits, self.router, self.bias, self.rep_off, self.rep_ids, buf=buf, stream=stream)
+        p.scatter(x, self.x_rows, buf=buf, stream=stream)
+        v, n = self.views[buf], T * p.k
+        ex.up(self.x_rows, v["offsets"], self.h, *self.kept[buf], rows=n, stream=stream)
+        ex.down(self.h, v["offsets"], v["ex_out"], rows=n, stream=stream)
+        y = p.combine(T, y, buf=buf, stream=stream)
+        self.saved[buf] = (x, logits)
+        return y
+
+    def backward(self, dy, dw13, dw2, dx=None, dlogits=None, accumulate=False, buf=0, stream=None):
+        p, ex = self.pool, self.experts
+        if not 0 <= buf < len(self.saved) or self.saved[buf] is None:
+            raise ValueError(f"set {buf} has no forward to go back through")
+        x, logits = self.saved[buf]
+        T, n, dev = x.shape[0], x.shape[0] * p.k, x.device
+        dx = torch.empty_like(x) if dx is None else dx
+        dlogits = torch.empty_like(logits) if dlogits is None else dlogits
+        moe._dense("dy", dy, torch.bfloat16, (T, p.H))
+        moe._dense("dx", dx, torch.bfloat16, (T, p.H))
+        moe._dense("dlogits", dlogits, torch.float32, (T, p.E))
+        ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
+        ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
+        offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
+        dgates = torch.empty((T, p.k), device=dev)
+        p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
+        hg = self.h  # the forward's h has been read
+        ex.down_backward(self.d_rows, codes, scales, self.row_gates, offsets, self.dgu, hg, self.parts, rows=n,
+                         stream=stream)
+        ex.down_grad(self.d_rows, hg, offsets, dw2, accumulate, rows=n, stream=stream)
+        ex.up_backward(self.dgu, offsets, self.d_rows, rows=n, stream=stream)  # d_rows now by x's side
+        p.scatter(x, self.x_rows, buf=buf, stream=stream)
+        ex.up_grad(self.dgu, self.x_rows, offsets, dw13, accumulate, rows=n, stream=stream)
+        p.gather(T, self.d_rows, dx, buf=buf, stream=stream)
+        routed = (None, None) if self.router is None else (self.router, logits)
+        p.gates_backward(T, self.parts, dgates, dlogits, *routed, buf=buf, stream=stream)
+        self.saved[buf] = None
+        return dx, dlogits
+
+    def check(self) -> int:
+        """Wait, and return the device error bits of the pool and the experts (0 = clean)."""
+        return self.pool.check() | self.experts.check()
+
+
 def random_experts(P, H, I, seed=0, device="cuda"):
     """Experts with N(0, 1 / inputs) weights, quantised per 128 x 128 block."""
     g = torch.Generator(device)

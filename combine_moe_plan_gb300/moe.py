@@ -24,6 +24,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SIZE", -3: "MOE_ERR_ALIG
           -9: "MOE_ERR_STATE"}
 DEVERR_REPLICA, DEVERR_DUPLICATE, DEVERR_SLOT, DEVERR_WINDOW, DEVERR_STALL = 0x1, 0x2, 0x4, 0x8, 0x10
 SCORES = {"softmax": 0, "sigmoid": 1}
+GRAD_F32, GRAD_F32_ADD, GRAD_BF16 = 0, 1, 2
 
 
 class LibraryMissing(ImportError):
@@ -66,6 +67,11 @@ class ExpertWeights(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("w13", "s13", "w2", "s2", "error_word")]
 
 
+class DenseWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("P", "H", "I")] + \
+               [(n, ctypes.c_void_p) for n in ("w13", "w2", "error_word")]
+
+
 _lib = None
 _lib_path = LIB_PATH
 
@@ -101,6 +107,15 @@ def lib() -> ctypes.CDLL:
         "moe_dispatch_f8": [vp, vp, i32, ctypes.c_int, vp],
         "moe_experts_up": [pp(ExpertWeights), vp, vp, i32, vp, i32, vp, vp, i32, vp],
         "moe_experts_down": [pp(ExpertWeights), vp, vp, i32, vp, i32, vp, vp],
+        "moe_scatter": [vp, vp, i32, vp, vp, ctypes.c_int, vp],
+        "moe_gather": [vp, vp, vp, i32, ctypes.c_int, vp],
+        "moe_gates_backward": [vp, pp(Router), vp, vp, i32, i32, vp, vp, ctypes.c_int, vp],
+        "moe_dense_up": [pp(DenseWeights), vp, vp, i32, vp, vp, vp, i32, vp],
+        "moe_dense_down": [pp(DenseWeights), vp, vp, i32, vp, vp],
+        "moe_dense_down_backward": [pp(DenseWeights), vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp],
+        "moe_dense_up_backward": [pp(DenseWeights), vp, vp, i32, vp, vp],
+        "moe_dense_up_grad": [pp(DenseWeights), vp, vp, vp, i32, vp, i32, vp],
+        "moe_dense_down_grad": [pp(DenseWeights), vp, vp, vp, i32, vp, i32, vp],
         "moe_dispatch": [vp, vp, i32, ctypes.c_int, vp],
         "moe_dispatch_after_plan": [vp, vp, i32, ctypes.c_int, vp],
         "moe_plan_dispatch": [vp, vp, i32, vp, vp, vp, ctypes.c_int, vp],
@@ -292,6 +307,43 @@ class Pool:
         _call("moe_combine", self.handle, _ptr(ex_out), _ptr(y), T, buf, _stream(stream))
         return y
 
+    def scatter(self, x, rows, row_gates=None, buf=0, stream=None):
+        """moe_scatter: bf16 ``x`` [T, H] into the set's windows of ``rows`` (at
+        least T * k rows), unquantized; ``row_gates`` fp32 [at least T * k] gets
+        each row's gate.  Both are returned."""
+        T, n = x.shape[0], x.shape[0] * self.k
+        _dense("x", x, torch.bfloat16, (T, self.H))
+        _tensor("rows", rows, torch.bfloat16, n, self.H)
+        if row_gates is not None:
+            _vector("row_gates", row_gates, n)
+        _on_one_gpu(self.workspace, x, rows, row_gates)
+        _call("moe_scatter", self.handle, _ptr(x), T, _ptr(rows), _ptr(row_gates), buf, _stream(stream))
+        return rows, row_gates
+
+    def gather(self, T, rows, y=None, buf=0, stream=None):
+        """moe_gather: ``y`` [T, H] = each token's k ``rows`` added up."""
+        _tensor("rows", rows, torch.bfloat16, T * self.k, self.H)
+        if y is None:
+            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.workspace.device)
+        _dense("y", y, torch.bfloat16, (T, self.H))
+        _on_one_gpu(self.workspace, rows, y)
+        _call("moe_gather", self.handle, _ptr(rows), _ptr(y), T, buf, _stream(stream))
+        return y
+
+    def gates_backward(self, T, gate_parts, dgates, dlogits, router=None, logits=None, buf=0, stream=None):
+        """moe_gates_backward: ``dgates`` [T, k] and ``dlogits`` [T, E] (fp32) from
+        the partial sums of ``DenseExperts.down_backward``; ``router`` and
+        ``logits`` are those of ``plan_routed``, and left out after ``plan``."""
+        parts = _tensor("gate_parts", gate_parts, torch.float32, T * self.k)
+        _dense("dgates", dgates, torch.float32, (T, self.k))
+        _dense("dlogits", dlogits, torch.float32, (T, self.E))
+        if logits is not None:
+            _dense("logits", logits, torch.float32, (T, self.E))
+        _on_one_gpu(self.workspace, gate_parts, dgates, dlogits, logits)
+        _call("moe_gates_backward", self.handle, None if router is None else ctypes.byref(router), _ptr(logits),
+              _ptr(gate_parts), parts, T, _ptr(dgates), _ptr(dlogits), buf, _stream(stream))
+        return dgates, dlogits
+
     def step_host(self, h_logits, h_x, h_y, h_ex_out=None, rep_off=None, rep_ids=None, buf=0, stream=None):
         """Whole layer from host tensors (pinned for asynchronous copies)."""
         _call("moe_step_host", self.handle, _ptr(h_logits), _ptr(h_x), _ptr(h_ex_out), _ptr(h_y),
@@ -413,8 +465,158 @@ class Experts:
         return int(self.error_word.item())
 
 
+class DenseExperts:
+    """The weights of P gated feed-forward experts in bf16, their products over
+    expert windows, and the gradients (moe_dense_*), for training.
+
+    w13 [P, 2 I, H] (gate rows, then up rows), w2 [P, H, I]; a product whose
+    weights are left out is refused.  The weights' gradients need none: without
+    any, ``sizes`` = (P, H, I).  ``rows``, in every call, is the number of rows the
+    windows lie in (None: all of the first tensor's).  ``check()`` returns the
+    device error word."""
+
+    def __init__(self, w13=None, w2=None, sizes=None, device="cuda"):
+        if sizes is None:
+            if w13 is None and w2 is None:
+                raise ValueError("give w13, w2, or sizes")
+            if (w13 if w13 is not None else w2).dim() != 3:
+                raise ValueError("weights have three dimensions: experts, outputs, inputs")
+            sizes = (w2.shape[0], w2.shape[1], w2.shape[2]) if w2 is not None else \
+                (w13.shape[0], w13.shape[2], w13.shape[1] // 2)
+        self.P, self.H, self.I = P, H, I = sizes
+        if H % 128 or I % 128:
+            raise ValueError(f"hidden and inner size are multiples of 128, got {H} and {I}")
+        for name, w, shape in (("w13", w13, (P, 2 * I, H)), ("w2", w2, (P, H, I))):
+            if w is not None:
+                _dense(name, w, torch.bfloat16, shape)
+                device = w.device
+        if w13 is not None and w2 is not None:
+            _on_one_gpu(w13, w2)
+        self.w13, self.w2 = w13, w2
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(self.error_word.device).synchronize()  # zero before any stream's kernels may set it
+        self.weights = DenseWeights(P, H, I, _ptr(w13), _ptr(w2), self.error_word.data_ptr())
+        self._ref = ctypes.byref(self.weights)
+
+    def kept(self, rows):
+        """Buffers for what ``up`` keeps of ``rows`` rows: E4M3 codes [rows, 2 I]
+        and fp32 scales [rows, 2 I / 128 rounded up to 4], neither filled."""
+        dev = self.error_word.device
+        return (torch.empty((rows, 2 * self.I), dtype=torch.float8_e4m3fn, device=dev),
+                torch.empty((rows, (self.I // 64 + 3) // 4 * 4), dtype=torch.float32, device=dev))
+
+    def up(self, x, offsets, h, codes=None, scales=None, rows=None, stream=None):
+        """h = bf16(silu(x gate^T) * (x up^T)) per window; with ``codes`` and
+        ``scales`` (``kept``) gate and up values are kept in 8 bits."""
+        rows = x.shape[0] if rows is None else rows
+        _tensor("x", x, torch.bfloat16, rows, self.H)
+        _tensor("h", h, torch.bfloat16, rows, self.I)
+        if (codes is None) != (scales is None):
+            raise ValueError("give both codes and scales, or neither")
+        stride = 0 if codes is None else self._codes(codes, scales, rows)
+        self._same_gpu(offsets, x, h, codes, scales)
+        _call("moe_dense_up", self._ref, _ptr(x), _ptr(offsets), rows, _ptr(h), _ptr(codes), _ptr(scales), stride,
+              _stream(stream))
+        return h
+
+    def down(self, h, offsets, out, rows=None, stream=None):
+        """out = bf16(h w2^T) per window."""
+        rows = h.shape[0] if rows is None else rows
+        _tensor("h", h, torch.bfloat16, rows, self.I)
+        _tensor("out", out, torch.bfloat16, rows, self.H)
+        self._same_gpu(offsets, h, out)
+        _call("moe_dense_down", self._ref, _ptr(h), _ptr(offsets), rows, _ptr(out), _stream(stream))
+        return out
+
+    def down_backward(self, dout, codes, scales, row_gates, offsets, dgu, hg, gate_parts, rows=None, stream=None):
+        """Back through w2, the rows' gates and the activation, at the values of
+        the codes: ``dgu`` [rows, 2 I] and ``hg`` [rows, I] (bf16), ``gate_parts``
+        [rows, I / 128] (fp32)."""
+        rows = dout.shape[0] if rows is None else rows
+        _tensor("dout", dout, torch.bfloat16, rows, self.H)
+        stride = self._codes(codes, scales, rows)
+        _vector("row_gates", row_gates, rows)
+        _tensor("dgu", dgu, torch.bfloat16, rows, 2 * self.I)
+        _tensor("hg", hg, torch.bfloat16, rows, self.I)
+        _tensor("gate_parts", gate_parts, torch.float32, rows, self.I // 128)
+        self._same_gpu(offsets, dout, codes, scales, row_gates, dgu, hg, gate_parts)
+        _call("moe_dense_down_backward", self._ref, _ptr(dout), _ptr(codes), _ptr(scales), stride, _ptr(row_gates),
+              _ptr(offsets), rows, _ptr(dgu), _ptr(hg), _ptr(gate_parts), _stream(stream))
+        return dgu, hg, gate_parts
+
+    def up_backward(self, dgu, offsets, dx, rows=None, stream=None):
+        """dx = bf16(dgu w13) per window."""
+        rows = dgu.shape[0] if rows is None else rows
+        _tensor("dgu", dgu, torch.bfloat16, rows, 2 * self.I)
+        _tensor("dx", dx, torch.bfloat16, rows, self.H)
+        self._same_gpu(offsets, dgu, dx)
+        _call("moe_dense_up_backward", self._ref, _ptr(dgu), _ptr(offsets), rows, _ptr(dx), _stream(stream))
+        return dx
+
+    def up_grad(self, dgu, x, offsets, dw13, accumulate=False, rows=None, stream=None):
+        """dw13[p] = sum of dgu^T x over window p, in fp32 or bf16 as ``dw13`` is;
+        with ``accumulate`` (fp32 only) added to what is there."""
+        return self._grad("moe_dense_up_grad", "dgu", dgu, 2 * self.I, "x", x, self.H, offsets, "dw13", dw13, accumulate,
+                          rows, stream)
+
+    def down_grad(self, dout, hg, offsets, dw2, accumulate=False, rows=None, stream=None):
+        """dw2[p] = sum of dout^T hg over window p; as ``up_grad``."""
+        return self._grad("moe_dense_down_grad", "dout", dout, self.H, "hg", hg, self.I, offsets, "dw2", dw2, accumulate,
+                          rows, stream)
+
+    def _grad(self, call, a_name, a, m, b_name, b, n, offsets, name, dw, accumulate, rows, stream):
+        rows = a.shape[0] if rows is None else rows
+        _tensor(a_name, a, torch.bfloat16, rows, m)
+        _tensor(b_name, b, torch.bfloat16, rows, n)
+        kind = self._gradient(name, dw, m, n, accumulate)
+        self._same_gpu(offsets, a, b, dw)
+        _call(call, self._ref, _ptr(a), _ptr(b), _ptr(offsets), rows, _ptr(dw), kind, _stream(stream))
+        return dw
+
+    def _gradient(self, name, dw, m, n, accumulate):
+        if dw.dtype not in (torch.float32, torch.bfloat16) or (accumulate and dw.dtype != torch.float32):
+            raise ValueError(f"{name}: want float32, or bfloat16 without accumulate, got {dw.dtype}")
+        _dense(name, dw, dw.dtype, (self.P, m, n))
+        return GRAD_BF16 if dw.dtype == torch.bfloat16 else GRAD_F32_ADD if accumulate else GRAD_F32
+
+    def _codes(self, codes, scales, rows):
+        _tensor("codes", codes, torch.float8_e4m3fn, rows, 2 * self.I)
+        return _tensor("scales", scales, torch.float32, rows)
+
+    def _same_gpu(self, offsets, *tensors):
+        if offsets.dtype != torch.int32 or offsets.shape != (self.P + 1,) or not offsets.is_contiguous():
+            raise ValueError(f"offsets: want a contiguous int32 tensor of {self.P + 1} values")
+        _on_one_gpu(self.error_word, offsets, *tensors)
+
+    def check(self, stream=None) -> int:
+        """Wait for ``stream`` and return the device error word (0 = clean)."""
+        (stream or torch.cuda.current_stream()).synchronize()
+        return int(self.error_word.item())
+
+
 def _on_gpu(t):
     return t.is_cuda
+
+
+def _on_current_gpu(t):
+    return t.is_cuda and t.device.index == _device()
+
+
+def _on_one_gpu(first, *others):
+    """Every tensor (None: left out) on the current GPU, which the kernels run on."""
+    if not _on_current_gpu(first):
+        raise ValueError(f"want every tensor on the current GPU, got a {first.dtype} {tuple(first.shape)} on {first.device}")
+    device = first.device
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"want every tensor on the current GPU, got a {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _vector(name, t, n):
+    """A contiguous fp32 vector of at least ``n`` values."""
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous float32 vector of at least {n} values, got "
+                         f"{'' if t.is_contiguous() else 'a strided '}{t.dtype} {tuple(t.shape)}")
 
 
 def _all_on_gpu(*tensors):

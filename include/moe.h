@@ -82,15 +82,15 @@ typedef enum moe_status {
     MOE_ERR_DEVICE = -7,    /* a kernel reported a bad index (error word) */
     MOE_ERR_REPLICA = -8,   /* malformed replica map (host check) */
     MOE_ERR_STATE = -9      /* T differs from the one planned for this set, or its
-                               codes are of another type than the call reads */
+                               codes or its plan are of another kind than the call reads */
 } moe_status;
 
 /* Device error-word bits (moe_pool_check). */
 #define MOE_DEVERR_REPLICA 0x1   /* replica map gave an id outside [0, P) */
 #define MOE_DEVERR_DUPLICATE 0x2 /* a token mapped twice to one physical expert */
 #define MOE_DEVERR_SLOT 0x4      /* a slot index outside [0, T*k) */
-#define MOE_DEVERR_WINDOW 0x8    /* an expert window outside the rows (moe_experts_*) */
-#define MOE_DEVERR_STALL 0x10    /* moe_experts_* gave up: a wait inside it ran out (its outputs are
+#define MOE_DEVERR_WINDOW 0x8    /* an expert window outside the rows (moe_experts_*, moe_dense_*) */
+#define MOE_DEVERR_STALL 0x10    /* moe_experts_* or moe_dense_* gave up: a wait inside it ran out (its outputs are
                                     void), or its shared memory is not as it expects (nothing done) */
 
 /*
@@ -395,6 +395,134 @@ MOE_API int moe_identity_experts(moe_pool* pool, int32_t T, int buf, void* strea
  */
 MOE_API int moe_combine(moe_pool* pool, const uint16_t* ex_out, uint16_t* y, int32_t T, int buf,
                         void* stream);
+
+/*
+ * ---- Training an expert layer ----
+ *
+ * The same routing, windows and pool, with bf16 experts and gradients.  Forward:
+ * moe_plan or moe_plan_routed, moe_scatter (x into the windows), moe_dense_up,
+ * moe_dense_down, moe_combine.  Kept for the backward pass: x, the plan, and of
+ * the experts' inside the gate and up values as 8-bit codes (moe_dense_up) -- not
+ * the dispatched rows, which moe_scatter makes again, nor the experts' outputs:
+ * with y = sum_j gate_j out_j the gradient of a gate is <dy, out_j> = <dy w2, h_j>,
+ * which moe_dense_down_backward has in hand.  Backward: moe_scatter (dy and the
+ * gates into the windows), moe_dense_down_backward, moe_dense_down_grad,
+ * moe_dense_up_backward, moe_dense_up_grad, moe_gather (dx), moe_gates_backward
+ * (the logits).  Sums are fp32 throughout, rounded once where a result is bf16; no
+ * result depends on the order in which CTAs run.  Rows of no window and NaN or
+ * infinities in them have no influence on any result.
+ */
+
+/*
+ * moe_scatter: token rows into the expert windows, unquantized ("AIV-Direct
+ * Write", for experts in bf16): rows[slot[t, j]] = x[t] for every j, and if
+ * row_gates is not NULL row_gates[slot[t, j]] = gates[t, j].
+ *   x     device bf16 [T, H]
+ *   rows  device bf16 [T*k (or more), H] out; row_gates fp32 [T*k (or more)] out
+ * Requires a prior plan on this set with the same T (T = 0: no-op).  Its gradient
+ * is moe_gather.
+ */
+MOE_API int moe_scatter(moe_pool* pool, const uint16_t* x, int32_t T, uint16_t* rows, float* row_gates, int buf,
+                        void* stream);
+
+/*
+ * moe_gather: y[t] = bf16(sum over j of rows[slot[t, j]]), fp32 in ascending j:
+ * moe_combine without gates, the gradient of moe_scatter.  Arguments, layout and
+ * errors as there.
+ */
+MOE_API int moe_gather(moe_pool* pool, const uint16_t* rows, uint16_t* y, int32_t T, int buf, void* stream);
+
+/*
+ * moe_gates_backward: gradients of the gates and of the router's logits from the
+ * partial sums of moe_dense_down_backward.
+ *   gate_parts  device fp32 [T*k (or more), parts], 1 <= parts <= 512
+ *   dgates      device fp32 [T, k] out: sum over b of gate_parts[slot[t, j], b]
+ *   dlogits     device fp32 [T, E] out, written whole
+ *   router, logits  the router and the fp32 [T, E] logits of this set's
+ *               moe_plan_routed; both NULL after moe_plan
+ * moe_plan: dl_j = g_j (dg_j - sum_i g_i dg_i) for the chosen experts, with the
+ * set's gates.  moe_plan_routed, S the sum of the token's chosen scores s_j: with
+ * renorm ds_j = scale / S (dg_j - sum_i dg_i s_i / S) (0 where S is 0), without
+ * ds_j = scale dg_j; sigmoid: dl_j = ds_j s_j (1 - s_j) for the chosen; softmax:
+ * dl_e = s_e (ds_e - sum_j ds_j s_j) for all experts, ds_e = 0 where not chosen.
+ * Which experts were chosen, and with them the balance bias and the groups, has no
+ * gradient.  MOE_ERR_STATE if the set was not planned with this T, or by the other
+ * kind of plan; T and the kind are those of the last plan called on the set,
+ * captured ones included.  T = 0: no-op.
+ */
+MOE_API int moe_gates_backward(moe_pool* pool, const moe_router* router, const float* logits, const float* gate_parts,
+                               int32_t parts, int32_t T, float* dgates, float* dlogits, int buf, void* stream);
+
+/*
+ * The experts' weights in bf16, in the layout of moe_experts: w13 [P, 2 I, H]
+ * (gate rows, then up rows), w2 [P, H, I].  Filled and kept by the caller; every
+ * pointer 16-byte aligned; error_word as there.  moe_dense_up and
+ * moe_dense_up_backward need w13 only, moe_dense_down and moe_dense_down_backward
+ * w2 only, the weights' gradients neither.
+ */
+typedef struct moe_dense {
+    int32_t P, H, I;
+    const uint16_t* w13;
+    const uint16_t* w2;
+    int32_t* error_word;
+} moe_dense;
+
+/*
+ * moe_dense_up: g, u = x * gate^T, x * up^T for every row of every expert window;
+ * h = bf16(g / (1 + exp(-g)) * u); and, unless codes and scales are NULL, g and u
+ * for the backward pass in 8 bits.
+ *   x [rows, H] bf16; h [rows, I] bf16 out
+ *   codes [rows, 2 I] E4M3 out (g, then u), scales [rows, scale_stride] fp32 out:
+ *         per row and 128 columns scale = max |v| / 448 and code = v * (448 / max |v|)
+ *         rounded to nearest even (all zero: scale 0, codes 0)
+ *   scale_stride  a multiple of 4 holding 2 I / 128 groups
+ *   offsets, rows  as moe_experts_up, which also says how bad windows are treated;
+ *         rows of no window are left as they are.  rows = 0: no-op.
+ */
+MOE_API int moe_dense_up(const moe_dense* experts, const uint16_t* x, const int32_t* offsets, int32_t rows,
+                         uint16_t* h, uint8_t* codes, float* scales, int32_t scale_stride, void* stream);
+
+/* moe_dense_down: out[r] = bf16(h[r] * w2[p]^T) for every row r of every window p
+ * (the rows moe_combine reads, "expert output return").  h [rows, I], out [rows, H]. */
+MOE_API int moe_dense_down(const moe_dense* experts, const uint16_t* h, const int32_t* offsets, int32_t rows,
+                           uint16_t* out, void* stream);
+
+/*
+ * moe_dense_down_backward: back through w2, the gates and the activation, from
+ * dout [rows, H] bf16, the gradient of y at each row's token (moe_scatter of dy),
+ * at the values that the codes stand for.  With d = dout[r] * w2[p] (fp32),
+ * g, u = codes * scales, s = 1 / (1 + exp(-g)), h = g s u:
+ *   gate_parts [rows, I / 128] fp32 out: sum over each 128 columns of d h
+ *   hg [rows, I] bf16 out: row_gates[r] h, for moe_dense_down_grad
+ *   dgu [rows, 2 I] bf16 out: row_gates[r] d u s (1 + g (1 - s)), then row_gates[r] d g s
+ *   row_gates [rows] fp32 (moe_scatter's); codes, scales, scale_stride, offsets, rows
+ *   as moe_dense_up
+ */
+MOE_API int moe_dense_down_backward(const moe_dense* experts, const uint16_t* dout, const uint8_t* codes,
+                                    const float* scales, int32_t scale_stride, const float* row_gates,
+                                    const int32_t* offsets, int32_t rows, uint16_t* dgu, uint16_t* hg,
+                                    float* gate_parts, void* stream);
+
+/* moe_dense_up_backward: dx[r] = bf16(dgu[r] * w13[p]) for every row r of every
+ * window p; moe_gather adds them up by token.  dgu [rows, 2 I], dx [rows, H]. */
+MOE_API int moe_dense_up_backward(const moe_dense* experts, const uint16_t* dgu, const int32_t* offsets, int32_t rows,
+                                  uint16_t* dx, void* stream);
+
+/*
+ * moe_dense_up_grad:   dw13[p] = sum over the rows r of window p of dgu[r]^T x[r]
+ * moe_dense_down_grad: dw2[p]  = sum over the rows r of window p of dout[r]^T hg[r]
+ *   dw13 [P, 2 I, H], dw2 [P, H, I]; grad: MOE_GRAD_F32, MOE_GRAD_F32_ADD (added to
+ *   what is there) or MOE_GRAD_BF16.  Every expert's gradient is written, zeros for
+ *   an empty (or bad) window, except with MOE_GRAD_F32_ADD, which leaves those.
+ *   rows = 0: every window must be empty, and offsets is not read.
+ */
+#define MOE_GRAD_F32 0
+#define MOE_GRAD_F32_ADD 1
+#define MOE_GRAD_BF16 2
+MOE_API int moe_dense_up_grad(const moe_dense* experts, const uint16_t* dgu, const uint16_t* x, const int32_t* offsets,
+                              int32_t rows, void* dw13, int32_t grad, void* stream);
+MOE_API int moe_dense_down_grad(const moe_dense* experts, const uint16_t* dout, const uint16_t* hg,
+                                const int32_t* offsets, int32_t rows, void* dw2, int32_t grad, void* stream);
 
 /*
  * One whole layer from HOST buffers: copy logits [T, E] and x [T, H] to the
