@@ -7,175 +7,592 @@
 //   up_back    dx = dgu w13
 //   grad       dw = a^T b over the rows of a window
 //
-// Simple form: a CTA computes 32 rows by 256 columns, a column a thread, sums in
-// fp32 registers, and finishes them from shared memory.
+// Mapping.  One persistent CTA per SM walks tiles of 128 by 256 outputs.  One
+// thread loads operands by TMA (64 inner elements a stage), one issues
+// tcgen05.mma (128 x 256 x 16) into one of two TMEM accumulators, eight warps
+// finish the tile in the other: they read it, do what the product ends in, and
+// send it out by TMA, each warp its own 32 rows in boxes of 128 bytes.
+//   Rows are the M operand of every product with weights.  Weights are read as
+// they lie: where the product runs over a row's inputs (up, down) they are a
+// K-major operand, where it runs over the outputs (down_back, up_back) an MN-major
+// one, and for grad both operands are: a window's rows are the inner dimension, of
+// any number.  There the last stage's rows past the window are cleared in shared
+// memory up to the next multiple of 16 (another expert's rows, or none: a NaN
+// there must not meet a zero), and the rest are left out.
+#include <cuda.h>
+
+#include "maps.h"
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "tc.cuh"
+#include "windows.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kMostExperts = 4096;
-constexpr int kTileM = 32, kTileN = 256;
+constexpr int kTileM = 128, kTileN = 256, kStepK = 64;
+constexpr int kRowBox = 32;                       // rows per TMA box of a row operand and of an output
+constexpr int kLine = 128;                        // bytes of a box's row
+constexpr int kABytes = kTileM * kLine;
+constexpr int kStageBytes = kABytes + kTileN * kLine;
+constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an MN-major operand
+constexpr int kSumWarps = 8;                      // warps that finish tiles
+constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
+constexpr int kDenseThreads = 32 * (kSumWarps + 2);
+constexpr int kStaging = kRowBox * kLine;         // of one warp
+constexpr int kMostStages = 4;
+constexpr int kSmemLimit = 227 * 1024;
+
+// The loading thread looks each tile up and leaves it in a ring for the other
+// warps.  It runs ahead of the last reader by at most the stages, the
+// accumulators and the tile being finished: every tile has at least one step.
+constexpr int kTileRing = 16;
 
 enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 
+struct alignas(16) Barriers {
+    uint64_t full[kMostStages], empty[kMostStages];  // stages
+    uint64_t acc_full[2], acc_empty[2];              // accumulators
+    uint64_t known[kTileRing];                       // tiles[i] is written
+    uint64_t drain;
+    // up .. up_back: expert, n, row, valid; grad: first row of dw, n, first row of the window, rows in it
+    int4 tiles[kTileRing];
+    uint32_t tmem;
+    int gave_up;
+    int warp_total[kDenseThreads / 32], warp_top[kDenseThreads / 32];
+};
+
+__host__ __device__ constexpr size_t smem_bytes(int stages, int P) {
+    return (size_t)stages * kStageBytes + kSumWarps * kStaging + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
+}
+static_assert(smem_bytes(3, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
+
 struct Problem {
-    int P, N, K;  // experts, outputs a row, inner size (of one half for up)
-    const uint16_t* a;
-    const uint16_t* w;
+    int P, N, K;  // experts, outputs a row, inner size; grad: columns of b and of a
     const int32_t* offsets;
     int rows;
-    uint16_t* out;      // up: h; down, up_back: the rows; down_back: hg
-    uint16_t* dgu;      // down_back
-    uint8_t* codes;     // up: out; down_back: in
+    uint16_t* out;     // up: h; down, up_back: the rows; down_back: hg
+    uint16_t* dgu;     // down_back
+    uint8_t* codes;    // up: out, or NULL; down_back: in
     float* scales;
     int scale_stride;
     const float* row_gates;
     float* parts;
     void* dw;
     int grad;
+    int stages;
     int32_t* err;
 };
 
-// Window p, if it lies inside the rows, runs forward and begins after every
-// earlier offset; otherwise empty and reported.
-__device__ __forceinline__ int2 window(const Problem& pr, int p) {
-    const int lo = pr.offsets[p], hi = pr.offsets[p + 1];
-    bool ok = lo >= 0 && hi >= lo && hi <= pr.rows;
-    for (int q = 0; q < p; ++q) ok = ok && pr.offsets[q] <= lo;
-    if (!ok && threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_WINDOW);
-    return ok ? make_int2(lo, hi) : make_int2(0, 0);
+// ---- finishing a tile: what one warp does with 32 rows by 128 columns ----
+
+// 32 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    uint32_t a[16], b[16];
+    tmem_load16(addr, a);
+    tmem_load16(addr + 16, b);
+    tmem_wait_load(a);
+    tmem_wait_load(b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]), v[16 + i] = __uint_as_float(b[i]);
 }
 
-__device__ __forceinline__ float bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)(pack_bf16x2_rn(v, 0.0f) & 0xffffu); }
-__device__ __forceinline__ float e4m3(uint8_t v) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-    float f;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"((uint16_t)(h & 0xffffu)));
+// A warp's box on its way out: 32 rows of 128 bytes in shared memory, 16-byte
+// chunk c of row r at c ^ (r mod 8) (the 128-byte swizzle: no bank conflicts when
+// a lane writes its row).
+struct Box {
+    unsigned char* staging;
+    int lane;
+
+    // The last box has been read, by TMA or by this warp.
+    __device__ __forceinline__ void begin() const {
+        if (elect_one()) bulk_wait_read();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void put(int chunk, uint4 v) const {
+        st_shared16(staging + lane * kLine + ((chunk ^ (lane & 7)) << 4), v);
+    }
+    // To (x, row) of the map: by TMA if all 32 rows are wanted, else the first
+    // `rows` of them 16 bytes a lane, to `at` and on by `pitch` bytes a row (a
+    // window ends here, and the next row is another expert's).
+    __device__ __forceinline__ void send(const CUtensorMap* map, int x, int row, int rows, void* at, size_t pitch) const {
+        fence_async_shared();
+        __syncwarp();
+        if (rows == kRowBox) {
+            if (elect_one()) {
+                tma_store_2d(map, x, row, staging);
+                bulk_commit();
+            }
+            __syncwarp();
+            return;
+        }
+        for (int i = lane; i < rows * 8; i += 32) {
+            const int r = i >> 3, c = i & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(staging + r * kLine + ((c ^ (r & 7)) << 4));
+            st16(static_cast<unsigned char*>(at) + r * pitch + c * 16, v);
+        }
+        __syncwarp();
+    }
+};
+
+// 32 values as bf16 into four chunks of a box.
+__device__ __forceinline__ void put_bf16(const Box& box, int chunk, const float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        box.put(chunk + i,
+                make_uint4(pack_bf16x2_rn(v[8 * i], v[8 * i + 1]), pack_bf16x2_rn(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16x2_rn(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2_rn(v[8 * i + 6], v[8 * i + 7])));
+}
+
+// Four E4M3 codes.
+__device__ __forceinline__ float4 unpack_e4m3(uint32_t w) {
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    float4 f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(lo));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.z), "=f"(f.w) : "r"(hi));
     return f;
 }
 
-template <Op OP>
-__global__ void __launch_bounds__(kTileN) dense_kernel(const Problem pr) {
-    __shared__ float a_tile[kTileM][33];
-    __shared__ float y[kTileM][kTileN];
-    grid_dependency_sync();
-    allow_dependents();
-    constexpr int kCols = OP == Op::kUp ? 128 : kTileN;  // outputs a tile
-    const int p = blockIdx.y, n0 = blockIdx.x * kCols, c = threadIdx.x;
-    const int2 win = window(pr, p);
-    const int half = c >> 7;  // up: 0 gate, 1 up
-    const int col = OP == Op::kUp ? n0 + (c & 127) : n0 + c;
-    const bool col_ok = col < pr.N;
-    const int groups = pr.N / 128;
-    // grad: the tile's rows are columns of a, and the window's rows the inner dimension
-    const int first = OP == Op::kGrad ? (int)blockIdx.z * kTileM : win.x;
-    const int last = OP == Op::kGrad ? first + kTileM : win.y;
-    const int K = OP == Op::kGrad ? win.y - win.x : pr.K;
-    const int M = pr.K;  // grad: columns of a
-    for (int m0 = first; m0 < last; m0 += kTileM) {
-        float acc[kTileM];
+// up: h from the gate columns (accumulator columns 0 ..) and the up columns (128 ..),
+// 64 of them by each half of the warps; then the codes, of g by one half and of u by
+// the other, so that a lane holds a whole group of its row.
+__device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
+                                          const Box& box, uint32_t acc, int half, int n, int row, int rows) {
+    box.begin();
 #pragma unroll
-        for (int r = 0; r < kTileM; ++r) acc[r] = 0.0f;
-        for (int k0 = 0; k0 < K; k0 += 32) {
-            __syncthreads();
-            for (int i = c; i < kTileM * 32; i += kTileN) {
-                float v = 0.0f;
-                if (OP == Op::kGrad) {
-                    const int kk = i / 32, r = i % 32;
-                    if (k0 + kk < K) v = bf16(pr.a[(size_t)(win.x + k0 + kk) * M + m0 + r]);
-                    a_tile[r][kk] = v;
-                } else {
-                    const int r = i / 32, kk = i % 32;
-                    if (m0 + r < last) v = bf16(pr.a[(size_t)(m0 + r) * K + k0 + kk]);
-                    a_tile[r][kk] = v;
-                }
-            }
-            __syncthreads();
-            for (int kk = 0; kk < 32 && k0 + kk < K; ++kk) {
-                const int k = k0 + kk;
-                float b = 0.0f;
-                if (col_ok) {
-                    if (OP == Op::kUp)
-                        b = bf16(pr.w[((size_t)p * 2 * pr.N + half * pr.N + col) * K + k]);
-                    else if (OP == Op::kDown)
-                        b = bf16(pr.w[((size_t)p * pr.N + col) * K + k]);
-                    else if (OP == Op::kGrad)
-                        b = bf16(pr.w[(size_t)(win.x + k) * pr.N + col]);
-                    else
-                        b = bf16(pr.w[((size_t)p * K + k) * pr.N + col]);
-                }
+    for (int c = 0; c < 2; ++c) {
+        float g[32], u[32];
+        tmem_load32(acc + half * 64 + c * 32, g);
+        tmem_load32(acc + kGroup + half * 64 + c * 32, u);
 #pragma unroll
-                for (int r = 0; r < kTileM; ++r) acc[r] = fmaf(a_tile[r][kk], b, acc[r]);
-            }
-        }
-        if (OP == Op::kGrad) {
-            if (!col_ok || (K == 0 && pr.grad == MOE_GRAD_F32_ADD)) continue;
+        for (int i = 0; i < 32; ++i) g[i] = gated(g[i], u[i]);
+        put_bf16(box, 4 * c, g);
+    }
+    const int x = n * kGroup + half * 64;
+    box.send(map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
+    if (pr.codes == nullptr) return;
+    acc += half * kGroup;
+    float amax = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kTileM; ++r) {
-                const size_t at = ((size_t)p * M + m0 + r) * pr.N + col;
-                if (pr.grad == MOE_GRAD_BF16)
-                    static_cast<uint16_t*>(pr.dw)[at] = to_bf16(acc[r]);
-                else
-                    static_cast<float*>(pr.dw)[at] = acc[r] + (pr.grad == MOE_GRAD_F32_ADD ? static_cast<float*>(pr.dw)[at] : 0.0f);
-            }
-            continue;
-        }
+    for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_load32(acc + c * 32, v);
 #pragma unroll
-        for (int r = 0; r < kTileM; ++r) y[r][c] = acc[r];
-        __syncthreads();
-        for (int r = 0; r < kTileM && m0 + r < last; ++r) {
-            const size_t row = m0 + r;
-            if (OP == Op::kDown || OP == Op::kUpBack) {
-                if (col_ok) pr.out[row * pr.N + col] = to_bf16(y[r][c]);
-            } else if (OP == Op::kUp) {
-                if (half == 0) {
-                    const float g = y[r][c], u = y[r][c + 128];
-                    pr.out[row * pr.N + col] = to_bf16(g / (1.0f + expf(-g)) * u);
-                }
-                if (pr.codes != nullptr) {
-                    float amax = 0.0f;
-                    for (int i = 0; i < 128; ++i) amax = fmaxf(amax, fabsf(y[r][half * 128 + i]));
-                    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
-                    const float inv = amax > 0.0f ? kE4M3Max / (amax * lift) : 0.0f;
-                    pr.codes[row * 2 * pr.N + half * pr.N + col] = (uint8_t)(pack_e4m3x2(y[r][c] * lift * inv, 0.0f) & 0xff);
-                    if ((c & 127) == 0) pr.scales[row * pr.scale_stride + half * groups + blockIdx.x] = amax / kE4M3Max;
-                }
-            } else if (col_ok) {
-                const float* sc = pr.scales + row * pr.scale_stride + col / 128;
-                const float g = e4m3(pr.codes[row * 2 * pr.N + col]) * sc[0];
-                const float u = e4m3(pr.codes[row * 2 * pr.N + pr.N + col]) * sc[groups];
-                const float s = 1.0f / (1.0f + expf(-g)), h = g * s * u, gate = pr.row_gates[row];
-                const float d = y[r][c], dh = gate * d;
-                pr.out[row * pr.N + col] = to_bf16(gate * h);
-                pr.dgu[row * 2 * pr.N + col] = to_bf16(dh * u * s * (1.0f + g * (1.0f - s)));
-                pr.dgu[row * 2 * pr.N + pr.N + col] = to_bf16(dh * g * s);
-                y[r][c] = d * h;
-            }
+        for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    }
+    // a tiny group is scaled up first, so that 448 / amax stays finite
+    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float inv = amax > 0.0f ? kE4M3Max / (amax * lift) : 0.0f;
+    box.begin();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float v[32];
+        tmem_load32(acc + c * 32, v);
+        uint32_t q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = pack_e4m3x2(v[4 * i] * lift * inv, v[4 * i + 1] * lift * inv) |
+                   pack_e4m3x2(v[4 * i + 2] * lift * inv, v[4 * i + 3] * lift * inv) << 16;
+        box.put(2 * c, make_uint4(q[0], q[1], q[2], q[3]));
+        box.put(2 * c + 1, make_uint4(q[4], q[5], q[6], q[7]));
+    }
+    const int xc = half * pr.N + n * kGroup;
+    box.send(map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
+    if (box.lane < rows)
+        pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] = amax / kE4M3Max;
+}
+
+// down, up_back, and grad in bf16: 128 columns of each half of the warps.
+__device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Box& box, uint32_t acc, int x, int row, int rows,
+                                            uint16_t* out, int width) {
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+        box.begin();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float v[32];
+            tmem_load32(acc + b * 64 + c * 32, v);
+            put_bf16(box, 4 * c, v);
         }
-        if (OP == Op::kDownBack) {
-            __syncthreads();
-            for (int i = c; i < kTileM * 2; i += kTileN) {
-                const int r = i >> 1, b = i & 1;
-                if (m0 + r < last && n0 + b * 128 < pr.N) {
-                    float sum = 0.0f;
-                    for (int j = 0; j < 128; ++j) sum += y[r][b * 128 + j];
-                    pr.parts[(size_t)(m0 + r) * groups + n0 / 128 + b] = sum;
+        box.send(map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
+    }
+}
+
+// down_back: a lane has one 128-group of its row, whose scales and sum are its own.
+__device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtensorMap* map_hg, const CUtensorMap* map_dgu,
+                                                 const Box& box, uint32_t acc, int blk, int row, int rows) {
+    const size_t mine = (size_t)row + max(0, min(box.lane, rows - 1));
+    const int groups = pr.N / kGroup;
+    const float gate = __ldg(pr.row_gates + mine);
+    const float sg = __ldg(pr.scales + mine * pr.scale_stride + blk);
+    const float su = __ldg(pr.scales + mine * pr.scale_stride + groups + blk);
+    const uint8_t* codes = pr.codes + mine * 2 * pr.N + blk * kGroup;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+        uint32_t du[32], hg[32];  // bf16 pairs of 64 columns
+        box.begin();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // 16 columns
+            const uint4 cg = __ldg(reinterpret_cast<const uint4*>(codes + b * 64 + c * 16));
+            const uint4 cu = __ldg(reinterpret_cast<const uint4*>(codes + pr.N + b * 64 + c * 16));
+            uint32_t d[16];
+            tmem_load16(acc + b * 64 + c * 16, d);
+            tmem_wait_load(d);
+            const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
+            uint32_t dg[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 fg = unpack_e4m3(wg[q]), fu = unpack_e4m3(wu[q]);
+                const float gs[4] = {fg.x, fg.y, fg.z, fg.w}, us[4] = {fu.x, fu.y, fu.z, fu.w};
+                float vg[4], vu[4], vh[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float g = gs[i] * sg, u = us[i] * su, dd = __uint_as_float(d[4 * q + i]);
+                    const float s = sigmoid(g), silu = g * s, h = silu * u, dh = gate * dd;
+                    sum += dd * h;
+                    vg[i] = dh * u * (s * (1.0f + g * (1.0f - s)));
+                    vu[i] = dh * silu;
+                    vh[i] = gate * h;
                 }
+                dg[2 * q] = pack_bf16x2_rn(vg[0], vg[1]), dg[2 * q + 1] = pack_bf16x2_rn(vg[2], vg[3]);
+                du[8 * c + 2 * q] = pack_bf16x2_rn(vu[0], vu[1]), du[8 * c + 2 * q + 1] = pack_bf16x2_rn(vu[2], vu[3]);
+                hg[8 * c + 2 * q] = pack_bf16x2_rn(vh[0], vh[1]), hg[8 * c + 2 * q + 1] = pack_bf16x2_rn(vh[2], vh[3]);
             }
+            box.put(2 * c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+            box.put(2 * c + 1, make_uint4(dg[4], dg[5], dg[6], dg[7]));
         }
+        const int x = blk * kGroup + b * 64;
+        const size_t wide = (size_t)2 * pr.N;
+        box.send(map_dgu, x, row, rows, pr.dgu + row * wide + x, wide * 2);
+        box.begin();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) box.put(c, make_uint4(du[4 * c], du[4 * c + 1], du[4 * c + 2], du[4 * c + 3]));
+        box.send(map_dgu, pr.N + x, row, rows, pr.dgu + row * wide + pr.N + x, wide * 2);
+        box.begin();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) box.put(c, make_uint4(hg[4 * c], hg[4 * c + 1], hg[4 * c + 2], hg[4 * c + 3]));
+        box.send(map_hg, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
+    }
+    if (box.lane < rows) pr.parts[mine * groups + blk] = sum;
+}
+
+// grad in fp32: 128 columns of each half of the warps, four boxes of 32.
+__device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Box& box, uint32_t acc, int x, int row, bool add) {
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        box.begin();
+        float v[32];
+        tmem_load32(acc + b * 32, v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            box.put(c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                  __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3])));
+        fence_async_shared();
+        __syncwarp();
+        if (elect_one()) {
+            if (add)
+                tma_add_2d(map, x + b * 32, row, box.staging);
+            else
+                tma_store_2d(map, x + b * 32, row, box.staging);
+            bulk_commit();
+        }
+        __syncwarp();
     }
 }
 
 template <Op OP>
-int launch_dense(const Problem& pr, int m_tiles, cudaStream_t s) {
-    constexpr int kCols = OP == Op::kUp ? 128 : kTileN;
-    const dim3 grid((unsigned)((pr.N + kCols - 1) / kCols), (unsigned)pr.P, (unsigned)m_tiles);
-    return launch_pdl(dense_kernel<OP>, grid, dim3(kTileN), 0, s, pr) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+__global__ void __launch_bounds__(kDenseThreads, 1)
+dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
+    constexpr bool kGrad = OP == Op::kGrad;
+    constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int stages = pr.stages;
+    // The kernel has no other shared memory, so the base lies on a 1024-byte
+    // boundary.  One that does not is refused.
+    if ((smem_u32(smem) & 1023u) != 0 || smem_bytes(stages, pr.P) > dynamic_smem_bytes()) {
+        grid_dependency_sync();  // no kernel behind this one starts before those in front of it are done
+        if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
+        return;
+    }
+    unsigned char* staging = smem + stages * kStageBytes;
+    Barriers& b = *reinterpret_cast<Barriers*>(staging + kSumWarps * kStaging);
+    int* first_m = reinterpret_cast<int*>(&b + 1);  // [P + 1]
+    volatile int* gave_up = &b.gave_up;
+    // Uniform in a warp, and through the shuffle known to be.
+    const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+    if (warp == kMmaWarp) {
+        if (lane == 0) {
+            for (int s = 0; s < stages; ++s) {
+                mbar_init(&b.full[s], 1);
+                mbar_init(&b.empty[s], 1);
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(&b.acc_full[s], 1);
+                mbar_init(&b.acc_empty[s], kSumWarps);
+            }
+            for (int i = 0; i < kTileRing; ++i) mbar_init(&b.known[i], 1);
+            mbar_init(&b.drain, 1);
+            b.gave_up = 0;
+            mbar_init_fence();
+        }
+        __syncwarp();
+        tmem_alloc_all(&b.tmem);
+        tc_fence_before();
+    } else if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        tma_prefetch_map(&map_out);
+        tma_prefetch_map(&map_out2);
+    }
+    grid_dependency_sync();
+    allow_dependents();
+    const int blocks = pr.N / kGroup;  // 128-blocks of outputs
+    const int n_tiles = OP == Op::kUp ? blocks : (blocks + 1) / 2;
+    // its barriers publish the above
+    const int m_total = scan_windows<kDenseThreads, kGrad ? kStepK : kTileM>(
+        pr.offsets, pr.P, pr.rows, pr.err, kGrad ? 1 : n_tiles, first_m, b.warp_total, b.warp_top, &b.tiles[0]);
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    // at most 2^31: checked by the host
+    const long long tiles = (long long)(kGrad ? pr.P * (pr.K / kTileM) : m_total) * n_tiles;
+
+    // Tile number j of this CTA, once the loading thread has left it in the ring.
+    const auto tile_written = [&](uint32_t j) {
+        return wait_written(MbarPhase{smem_u32(&b.known[j % kTileRing]), (j / kTileRing) & 1}, gave_up);
+    };
+    const auto tile_at = [&](uint32_t j) { return *const_cast<const int4*>(&b.tiles[j % kTileRing]); };
+    // Steps of a tile along the inner dimension.  A window without rows has one,
+    // of zeros (past the end of the rows), so that its gradient is zeros like any other's.
+    const auto steps_of = [&](const int4& t) { return kGrad ? max(1, (t.w + kStepK - 1) / kStepK) : pr.K / kStepK; };
+
+    if (warp == kTmaWarp) {
+        if (elect_one()) {
+            int s = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            TileWalk<kTileM> walk;
+            uint32_t j = 0;
+            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+                // no tile is written any more, so none overwrites one that a
+                // warp which runs on without waiting is reading
+                if (!(ok = ok && *gave_up == 0)) break;
+                int4 t;
+                int b_row = 0, m0 = 0;
+                if constexpr (kGrad) {
+                    const int m_tiles = pr.K / kTileM, mn = (int)tile / n_tiles, p = mn / m_tiles;
+                    m0 = (mn - p * m_tiles) * kTileM;
+                    const int lo = pr.offsets[p], count = first_m[p + 1] > first_m[p] ? pr.offsets[p + 1] - lo : 0;
+                    t = make_int4(p * pr.K + m0, (int)tile - mn * n_tiles, count > 0 ? lo : pr.rows, count);
+                } else {
+                    if (j == 0) {
+                        t = b.tiles[0];
+                        walk.p = t.x;
+                    } else {
+                        const Tile w = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                        t = make_int4(w.p, w.n, w.row, w.valid);
+                    }
+                    b_row = kBMn ? t.x * pr.K : t.x * (OP == Op::kUp ? 2 : 1) * pr.N + t.y * (OP == Op::kUp ? kGroup : kTileN);
+                }
+                if (kGrad || j > 0) b.tiles[j % kTileRing] = t;
+                mbar_arrive(&b.known[j % kTileRing]);
+                const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
+                const int steps = steps_of(t);
+                const int boxes = kGrad ? kTileM / kStepK : (t.w + kRowBox - 1) / kRowBox;
+                const uint32_t bytes = (kGrad ? kABytes : boxes * kStaging) + (two ? 2 : 1) * kGroup * kLine;
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
+                    unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
+                    uint64_t* bar = &b.full[s];
+                    mbar_expect_tx(bar, bytes);
+                    if constexpr (kBMn) {
+                        const int y = kGrad ? t.z + k * kStepK : b_row + k * kStepK;
+                        for (int i = 0; i < (two ? 4 : 2); ++i)
+                            tma_load_2d(pb + i * kBlockBytes, &map_b, t.y * kTileN + i * kStepK, y, bar);
+                    } else {
+                        tma_load_2d(pb, &map_b, k * kStepK, b_row, bar);
+                        if (two)
+                            tma_load_2d(pb + kGroup * kLine, &map_b, k * kStepK, b_row + (OP == Op::kUp ? pr.N : kGroup), bar);
+                    }
+                    if constexpr (kGrad) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(pa + i * kBlockBytes, &map_a, m0 + i * kStepK, t.z + k * kStepK, bar);
+                    } else {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(pa + i * kStaging, &map_a, k * kStepK, t.z + i * kRowBox, bar);
+                    }
+                    ++issued;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
+            // Leave only after the copies in flight have landed (or never will),
+            // also where this thread was through before another wait gave up.
+            const uint64_t t0 = now_ns();
+            for (uint32_t i = issued > (uint32_t)stages ? issued - stages : 0; i < issued; ++i)
+                while (!mbar_try(smem_u32(&b.full[i % stages]), (i / stages) & 1) && now_ns() - t0 < kStallNs) {
+                }
+        }
+    } else if (warp == kMmaWarp) {
+        bool ok = true;
+        const uint64_t desc_a = kGrad ? umma_desc_mn(smem, kBlockBytes) : umma_desc(smem);
+        const uint64_t desc_b = kBMn ? umma_desc_mn(smem + kABytes, kBlockBytes) : umma_desc(smem + kABytes);
+        // From one 16 of the inner dimension to the next: 32 bytes along a row, or 16 rows.
+        constexpr uint32_t kNextA = kGrad ? 16 * kLine / 16 : 2, kNextB = kBMn ? 16 * kLine / 16 : 2;
+        uint32_t j = 0, done = 0;  // tiles and steps of this CTA
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+            if (!(ok = __all_sync(kFull, tile_written(j)))) break;
+            const int4 t = tile_at(j);
+            const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
+            const uint32_t idesc = umma_idesc_bf16(kTileM, two ? kTileN : kGroup, kGrad, kBMn);
+            const uint32_t buf = j & 1, d = tmem + buf * kTileN;
+            const int steps = steps_of(t), whole = kGrad ? t.w / kStepK : steps;
+            if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_empty[buf], ((j >> 1) & 1) ^ 1, gave_up)))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                uint32_t s = done % stages, phase = (done / stages) & 1;
+                for (int k = 0; k < whole; ++k) {
+                    if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
+                    tc_fence_after();
+                    const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
+#pragma unroll
+                    for (int i = 0; i < kStepK / 16; ++i)
+                        umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > 0 || i > 0);
+                    umma_commit(&b.empty[s]);
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (ok && whole == steps) umma_commit(&b.acc_full[buf]);
+            }
+            if (!(ok = __all_sync(kFull, ok))) break;
+            if (kGrad && whole < steps) {
+                // The window's last rows: cleared behind them up to a multiple of 16.
+                const uint32_t last = done + whole, s = last % stages, phase = (last / stages) & 1;
+                if (!(ok = __all_sync(kFull, mbar_wait(&b.full[s], phase, gave_up)))) break;
+                const int valid = t.w - whole * kStepK, up = max(16, (valid + 15) & ~15);
+                const int chunks = (up - valid) * 8;
+                for (int i = lane; valid > 0 && i < (two ? 6 : 4) * chunks; i += 32) {  // 64-element blocks of A, then of B
+                    const int blk = i / chunks, at = i - blk * chunks;
+                    st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (elect_one()) {
+                    tc_fence_after();
+                    const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
+                    for (int i = 0; i < up / 16; ++i)
+                        umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, whole > 0 || i > 0);
+                    umma_commit(&b.empty[s]);
+                    umma_commit(&b.acc_full[buf]);
+                }
+                __syncwarp();
+            }
+            done += steps;
+        }
+        if (elect_one()) {
+            if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
+            umma_commit(&b.drain);  // leave only after the products in flight
+            const uint64_t t0 = now_ns();
+            while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
+            }
+        }
+    } else {
+        // Finishing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
+        // lane) and one half of the tile's columns.
+        const int quarter = warp & 3, half = warp >> 2;
+        const Box box = {staging + warp * kStaging, lane};
+        uint32_t j = 0;
+        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+            if (!__all_sync(kFull, tile_written(j))) break;
+            const int4 t = tile_at(j);
+            const uint32_t buf = j & 1;
+            if (!__all_sync(kFull, mbar_wait(&b.acc_full[buf], (j >> 1) & 1, gave_up))) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTileN;
+            const int row = (kGrad ? t.x : t.z) + quarter * 32;
+            const int rows = kGrad ? kRowBox : max(0, min(kRowBox, t.w - quarter * 32));
+            const int blk = 2 * t.y + half;  // this half's 128 columns (up: of another kind)
+            if constexpr (OP == Op::kUp) {
+                if (rows > 0) finish_up(pr, &map_out, &map_out2, box, acc, half, t.y, row, rows);
+            } else if (rows > 0 && blk < blocks) {
+                const uint32_t mine = acc + half * kGroup;
+                if constexpr (OP == Op::kDownBack)
+                    finish_down_back(pr, &map_out, &map_out2, box, mine, blk, row, rows);
+                else if constexpr (!kGrad)
+                    finish_rows(&map_out, box, mine, blk * kGroup, row, rows, pr.out, pr.N);
+                else if (pr.grad == MOE_GRAD_BF16)
+                    finish_rows(&map_out, box, mine, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
+                else if (pr.grad == MOE_GRAD_F32 || t.w > 0)
+                    finish_grad(&map_out, box, mine, blk * kGroup, row, pr.grad == MOE_GRAD_F32_ADD);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&b.acc_empty[buf]);
+        }
+        if (elect_one()) bulk_wait();
+        __syncwarp();
+        if (*gave_up && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ---- host side ----
+
+constexpr CUtensorMapDataType kByte = CU_TENSOR_MAP_DATA_TYPE_UINT8, kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+
+template <Op OP>
+int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t s) {
+    constexpr bool kGrad = OP == Op::kGrad;
+    constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;
+    const int blocks = pr.N / kGroup, n_tiles = OP == Op::kUp ? blocks : (blocks + 1) / 2;
+    // The most tiles any windows over these rows can have.
+    const long long m_most = kGrad ? (long long)pr.P * (pr.K / kTileM)
+                                   : ((long long)pr.rows + kTileM - 1) / kTileM + min(pr.P, pr.rows);
+    if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
+    const size_t rows = (size_t)pr.rows, n_rows = (size_t)pr.P * pr.N, k_rows = (size_t)pr.P * pr.K;
+    CUtensorMap map_a, map_b, map_out, map_out2;
+    bool ok = tile_map(&map_a, kBf16, a, rows, pr.K, kGrad ? kStepK : kRowBox);
+    ok = ok && (kGrad  ? tile_map(&map_b, kBf16, w, rows, pr.N, kStepK)
+                : kBMn ? tile_map(&map_b, kBf16, w, k_rows, pr.N, kStepK)
+                       : tile_map(&map_b, kBf16, w, (OP == Op::kUp ? 2 : 1) * n_rows, pr.K, kGroup));
+    if (kGrad)
+        ok = ok && tile_map(&map_out, pr.grad == MOE_GRAD_BF16 ? kBf16 : kF32, pr.dw, k_rows, pr.N, kRowBox);
+    else
+        ok = ok && tile_map(&map_out, kBf16, pr.out, rows, pr.N, kRowBox);
+    map_out2 = map_out;
+    if (OP == Op::kUp && pr.codes != nullptr) ok = ok && tile_map(&map_out2, kByte, pr.codes, rows, 2 * pr.N, kRowBox);
+    if (OP == Op::kDownBack) ok = ok && tile_map(&map_out2, kBf16, pr.dgu, rows, 2 * pr.N, kRowBox);
+    if (!ok) return MOE_ERR_CUDA;
+    // Four stages where the prefix of the windows leaves room for them (607 experts and fewer).
+    pr.stages = smem_bytes(kMostStages, pr.P) <= kSmemLimit ? kMostStages : kMostStages - 1;
+    // The same limit for every size, so that callers on several threads do not lower it for each other.
+    if (cudaFuncSetAttribute(dense_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int sms = sm_count();
+    if (sms < 1) return MOE_ERR_CUDA;
+    const unsigned grid = (unsigned)(m_most * n_tiles < sms ? m_most * n_tiles : sms);
+    return launch_pdl(dense_kernel<OP>, dim3(grid), dim3(kDenseThreads), smem_bytes(pr.stages, pr.P), s, map_a, map_b,
+                      map_out, map_out2, pr) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -217,9 +634,9 @@ int grad_call(const moe_dense* e, int M, int N, const uint16_t* a, const uint16_
         return cudaMemsetAsync(dw, 0, bytes, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     Problem pr = {};
-    pr.P = e->P, pr.N = N, pr.K = M, pr.a = a, pr.w = b, pr.offsets = offsets, pr.rows = rows;
+    pr.P = e->P, pr.N = N, pr.K = M, pr.offsets = offsets, pr.rows = rows;
     pr.dw = dw, pr.grad = grad, pr.err = e->error_word;
-    return launch_dense<Op::kGrad>(pr, M / kTileM, s);
+    return launch_dense<Op::kGrad>(pr, a, b, s);
 }
 
 }  // namespace
@@ -237,9 +654,9 @@ extern "C" MOE_API int moe_dense_up(const moe_dense* e, const uint16_t* x, const
                           keep ? scales : static_cast<const void*>(h)};
     if ((rc = check_pointers(need, rows)) != MOE_OK || rows == 0) return rc;
     Problem pr = {};
-    pr.P = e->P, pr.N = e->I, pr.K = e->H, pr.a = x, pr.w = e->w13, pr.offsets = offsets, pr.rows = rows, pr.out = h;
+    pr.P = e->P, pr.N = e->I, pr.K = e->H, pr.offsets = offsets, pr.rows = rows, pr.out = h;
     pr.codes = codes, pr.scales = scales, pr.scale_stride = scale_stride, pr.err = e->error_word;
-    return launch_dense<Op::kUp>(pr, 1, static_cast<cudaStream_t>(stream));
+    return launch_dense<Op::kUp>(pr, x, e->w13, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" MOE_API int moe_dense_down(const moe_dense* e, const uint16_t* h, const int32_t* offsets, int32_t rows,
@@ -249,9 +666,9 @@ extern "C" MOE_API int moe_dense_down(const moe_dense* e, const uint16_t* h, con
     const void* need[] = {e->w2, h, offsets, out};
     if ((rc = check_pointers(need, rows)) != MOE_OK || rows == 0) return rc;
     Problem pr = {};
-    pr.P = e->P, pr.N = e->H, pr.K = e->I, pr.a = h, pr.w = e->w2, pr.offsets = offsets, pr.rows = rows, pr.out = out;
+    pr.P = e->P, pr.N = e->H, pr.K = e->I, pr.offsets = offsets, pr.rows = rows, pr.out = out;
     pr.err = e->error_word;
-    return launch_dense<Op::kDown>(pr, 1, static_cast<cudaStream_t>(stream));
+    return launch_dense<Op::kDown>(pr, h, e->w2, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" MOE_API int moe_dense_down_backward(const moe_dense* e, const uint16_t* dout, const uint8_t* codes,
@@ -264,10 +681,10 @@ extern "C" MOE_API int moe_dense_down_backward(const moe_dense* e, const uint16_
     const void* need[] = {e->w2, dout, codes, scales, row_gates, offsets, dgu, hg, gate_parts};
     if ((rc = check_pointers(need, rows)) != MOE_OK || rows == 0) return rc;
     Problem pr = {};
-    pr.P = e->P, pr.N = e->I, pr.K = e->H, pr.a = dout, pr.w = e->w2, pr.offsets = offsets, pr.rows = rows;
+    pr.P = e->P, pr.N = e->I, pr.K = e->H, pr.offsets = offsets, pr.rows = rows;
     pr.out = hg, pr.dgu = dgu, pr.codes = const_cast<uint8_t*>(codes), pr.scales = const_cast<float*>(scales);
     pr.scale_stride = scale_stride, pr.row_gates = row_gates, pr.parts = gate_parts, pr.err = e->error_word;
-    return launch_dense<Op::kDownBack>(pr, 1, static_cast<cudaStream_t>(stream));
+    return launch_dense<Op::kDownBack>(pr, dout, e->w2, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" MOE_API int moe_dense_up_backward(const moe_dense* e, const uint16_t* dgu, const int32_t* offsets,
@@ -277,9 +694,9 @@ extern "C" MOE_API int moe_dense_up_backward(const moe_dense* e, const uint16_t*
     const void* need[] = {e->w13, dgu, offsets, dx};
     if ((rc = check_pointers(need, rows)) != MOE_OK || rows == 0) return rc;
     Problem pr = {};
-    pr.P = e->P, pr.N = e->H, pr.K = 2 * e->I, pr.a = dgu, pr.w = e->w13, pr.offsets = offsets, pr.rows = rows;
+    pr.P = e->P, pr.N = e->H, pr.K = 2 * e->I, pr.offsets = offsets, pr.rows = rows;
     pr.out = dx, pr.err = e->error_word;
-    return launch_dense<Op::kUpBack>(pr, 1, static_cast<cudaStream_t>(stream));
+    return launch_dense<Op::kUpBack>(pr, dgu, e->w13, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" MOE_API int moe_dense_up_grad(const moe_dense* e, const uint16_t* dgu, const uint16_t* x,

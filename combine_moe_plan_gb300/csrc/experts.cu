@@ -43,10 +43,12 @@
 // a time (345 / 336).
 #include <cuda.h>
 
+#include "maps.h"
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "tc.cuh"
+#include "windows.cuh"
 
 namespace moe {
 namespace {
@@ -119,120 +121,9 @@ struct Problem {
     int32_t* err;
 };
 
-// A tile: kTileM rows of one expert's window (from `row`, `valid` of them) by
-// two 128-blocks of its weight rows: UP: gate block n and up block n; down:
-// blocks 2n and 2n + 1 (the last one alone where their number is odd).
-struct Tile {
-    int p, n, row, valid;
-};
-
-// Tiles in the order (expert, n, rows), rows fastest: CTAs working side by
-// side share a block of weights.  first_m[p] counts the row tiles before
-// expert p; the expert is found by bisection from the last one on (tile indices
-// only grow), not step by step: a few rows over hundreds of experts leave most
-// of them empty (walking past them took 2 us of a single token's 46).
-struct TileWalk {
-    int p = 0;
-    __device__ __forceinline__ Tile at(int tile, int n_tiles, const int* first_m, const int32_t* offsets,
-                                       int P) {
-        const int m_index = tile / n_tiles;
-        if (first_m[p + 1] <= m_index) {
-            int past = P;
-            while (past - p > 1) {
-                const int mid = (p + past) >> 1;
-                if (first_m[mid] <= m_index)
-                    p = mid;
-                else
-                    past = mid;
-            }
-        }
-        const int m_tiles = first_m[p + 1] - first_m[p];
-        const int local = tile - first_m[p] * n_tiles;
-        Tile t;
-        t.p = p;
-        t.n = local / m_tiles;
-        const int lo = offsets[p], hi = offsets[p + 1];
-        t.row = lo + (local - t.n * m_tiles) * kTileM;
-        t.valid = min(kTileM, hi - t.row);
-        return t;
-    }
-};
-
-// First row tile of every expert, in shared memory; returns their number.  A
-// window that leaves the rows, runs backwards or starts before an earlier
-// offset (it could share rows with an earlier window) counts as empty and is
-// reported.  The thread that holds the expert of the CTA's first tile leaves
-// that tile in *first (the loading thread need not look it up).  Whole CTA.
-__device__ __forceinline__ int scan_windows(const Problem& pr, int n_tiles, int* first_m, int* warp_total,
-                                            int* warp_top, int4* first) {
-    constexpr int kWarps = kExpertsThreads / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (pr.P + kExpertsThreads - 1) / kExpertsThreads;
-    const int lo = min(pr.P, (int)threadIdx.x * per), hi = min(pr.P, lo + per);
-    // With an expert a thread at most (P <= 384) its offsets are read once.
-    const int a0 = lo < hi ? pr.offsets[lo] : 0, b0 = lo < hi ? pr.offsets[lo + 1] : 0;
-    // the largest offset before this thread's first
-    int top = a0;
-    for (int p = lo + 1; p < hi; ++p) top = max(top, pr.offsets[p]);
-    int incl = top;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off) incl = max(incl, o);
-    }
-    if (lane == 31) warp_top[warp] = incl;
-    top = __shfl_up_sync(kFull, incl, 1);
-    if (lane == 0) top = 0;
-    __syncthreads();
-    top = max(top, __reduce_max_sync(kFull, lane < warp ? warp_top[lane] : 0));
-
-    int sum = 0;
-    for (int p = lo; p < hi; ++p) {
-        const int a = p == lo ? a0 : pr.offsets[p], b = p == lo ? b0 : pr.offsets[p + 1];
-        const bool ok = a >= top && b >= a && b <= pr.rows;
-        top = max(top, a);
-        if (!ok && blockIdx.x == 0) set_error(pr.err, MOE_DEVERR_WINDOW);
-        const int m = ok ? (b - a + kTileM - 1) / kTileM : 0;
-        first_m[p] = m;
-        sum += m;
-    }
-    incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off) incl += o;
-    }
-    if (lane == 31) warp_total[warp] = incl;
-    __syncthreads();
-    const int mine = lane < kWarps ? warp_total[lane] : 0;
-    const int total = __reduce_add_sync(kFull, mine);
-    int run = __reduce_add_sync(kFull, lane < warp ? mine : 0) + incl - sum;
-    const int m_first = (int)blockIdx.x / n_tiles;
-    for (int p = lo; p < hi; ++p) {
-        const int m = first_m[p];
-        first_m[p] = run;
-        if (m_first >= run && m_first < run + m) {
-            const int a = p == lo ? a0 : pr.offsets[p], b = p == lo ? b0 : pr.offsets[p + 1];
-            const int local = (int)blockIdx.x - run * n_tiles, n = local / m, row = a + (local - n * m) * kTileM;
-            *first = make_int4(p, n, row, min(kTileM, b - row));
-        }
-        run += m;
-    }
-    if (threadIdx.x == 0) first_m[pr.P] = total;
-    __syncthreads();
-    return total;
-}
-
-// g / (1 + exp(-g)) * u.  exp by 2^t with t = -g log2(e): the rounding of t
-// makes its relative error |g| 2^-24, next to 2^-22 for the approximations;
-// where |g| is large either exp(-g) or the whole product is negligible.  An
-// overflow gives the limit 0.
-__device__ __forceinline__ float gated(float g, float u) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
-}
+// A tile is by two 128-blocks of its expert's weight rows: UP: gate block n and
+// up block n; down: blocks 2n and 2n + 1 (the last one alone where their number
+// is odd).
 
 template <bool UP>
 __global__ void __launch_bounds__(kExpertsThreads, 1)
@@ -290,7 +181,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int blocks = pr.N / kGroup;                       // 128-blocks of outputs
     const int n_tiles = UP ? blocks : (blocks + 1) / 2;
     // its barriers publish the above
-    const int m_total = scan_windows(pr, n_tiles, first_m, b.warp_total, b.warp_top, &b.tiles[0]);
+    const int m_total = scan_windows<kExpertsThreads, kTileM>(pr.offsets, pr.P, pr.rows, pr.err, n_tiles, first_m,
+                                                              b.warp_total, b.warp_top, &b.tiles[0]);
     tc_fence_after();
     const uint32_t tmem = b.tmem;
 
@@ -323,7 +215,7 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             uint32_t phase = 0, issued = 0;
             uint32_t used = 0x04040404u * (kTileM / kRowBox / 4);  // boxes holding something, 8 bits a buffer
             bool ok = true;
-            TileWalk walk;
+            TileWalk<kTileM> walk;
             uint32_t j = 0;
             for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
                 // no tile is written any more, so none overwrites one that a
@@ -615,51 +507,6 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 }
 
 // ---- host side ----
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled through the runtime (no driver library is linked);
-// NULL if there is none.  Looked up once.
-EncodeTiledFn encode_tiled() {
-    static const EncodeTiledFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            f = nullptr;
-        }
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    return fn;
-}
-
-// A map of a dense [rows, width] tensor of bytes or bf16, in boxes of box_rows x
-// 128 bytes, 128-byte swizzle; a load reads zeros past the end.
-bool tile_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, size_t rows, int width, int box_rows) {
-    const EncodeTiledFn encode = encode_tiled();
-    if (encode == nullptr) return false;
-    const int size = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * size};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, steps[2] = {1, 1};
-    return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// SMs of the current device (0: none).
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return 0;
-    }
-    return sms;
-}
 
 template <bool UP>
 int launch_experts(const Problem& pr, const uint8_t* a, const uint8_t* w, cudaStream_t s) {

@@ -1,6 +1,6 @@
 // tc.cuh -- inline PTX for the fifth-generation tensor cores (tcgen05), their
-// memory (TMEM), TMA tile loads and mbarriers, as the experts' products use
-// them.
+// memory (TMEM), TMA tile loads and mbarriers, as the experts' products (E4M3
+// and bf16) use them.
 #pragma once
 
 #include <cstdint>
@@ -113,6 +113,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y,
                  "r"(y), "r"(smem_u32(src))
                  : "memory");
 }
+// The same box of fp32, added to what is there (each element once).
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int x, int y, const void* src) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's stores have read shared memory / are complete.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -184,6 +190,29 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        : "memory");
+}
+// ---- tcgen05.mma, kind::f16 (bf16 x bf16, fp32 accumulators) ----
+// An operand whose rows are the inner dimension ("MN-major"): blocks of 64
+// elements of the outer dimension (128 bytes, 128-byte swizzle), the inner
+// dimension's rows below one another, 8-row groups 1024 bytes apart (bits 32-45)
+// and blocks `block_bytes` apart (bits 16-29).
+__device__ __forceinline__ uint64_t umma_desc_mn(const void* smem, uint32_t block_bytes) {
+    return (uint64_t)((smem_u32(smem) & 0x3ffffu) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) | (64ull << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// As umma_idesc_e4m3, with A and B bf16 (bits 7-9 and 10-12 = 1) and their
+// majors (bits 15 and 16: 1 = MN-major).
+__host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(n / 8) << 17) | ((uint32_t)(m / 16) << 24);
+}
+__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
         : "memory");
 }
 // Arrive on `bar` when every tcgen05 operation this thread issued is done.
