@@ -40,7 +40,10 @@ constexpr int kStageBytes = kABytes + kTileN * kLine;
 constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an MN-major operand
 constexpr int kSumWarps = 8;                      // warps that finish tiles
 constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
-constexpr int kDenseThreads = 32 * (kSumWarps + 2);
+constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // three warpgroups
+// Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
+// 256 x 216 + 128 x 72 = 64,512.
+constexpr int kSumRegs = 216, kOtherRegs = 72;
 constexpr int kStaging = kRowBox * kLine;         // of one warp
 constexpr int kMostStages = 4;
 constexpr int kSmemLimit = 227 * 1024;
@@ -52,6 +55,14 @@ constexpr int kTileRing = 16;
 
 enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 
+// Steps that are summed in TMEM before the sums go to registers.  The tensor cores
+// cut their sums off instead of rounding them, which shortens a sum by about
+// 2.4e-8 of it for every 16 terms (98,304 rows over 64 windows: 2.3e-6).  Results
+// in fp32 (a gradient, a scale, a gate's parts) are therefore summed 256 terms at a
+// time, and those sums added up in registers, rounded to nearest; results in bf16
+// have no use for it.
+__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 4; }
+
 struct alignas(16) Barriers {
     uint64_t full[kMostStages], empty[kMostStages];  // stages
     uint64_t acc_full[2], acc_empty[2];              // accumulators
@@ -62,6 +73,7 @@ struct alignas(16) Barriers {
     uint32_t tmem;
     int gave_up;
     int warp_total[kDenseThreads / 32], warp_top[kDenseThreads / 32];
+    float maxima[2][2][kTileM];  // up: of gate and up columns, of the two halves of each row
 };
 
 __host__ __device__ constexpr size_t smem_bytes(int stages, int P) {
@@ -88,15 +100,33 @@ struct Problem {
 
 // ---- finishing a tile: what one warp does with 32 rows by 128 columns ----
 
-// 32 columns of this warp's lanes.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-    uint32_t a[16], b[16];
-    tmem_load16(addr, a);
-    tmem_load16(addr + 16, b);
-    tmem_wait_load(a);
-    tmem_wait_load(b);
+// A lane's 128 sums, in pairs: of its row 64 columns from accumulator column c0
+// and 64 from c1.
+struct Sums {
+    uint64_t v[64];
+    __device__ __forceinline__ float2 at(int pair) const { return unpack2(v[pair]); }
+};
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <bool FIRST>
+__device__ __forceinline__ void take_sums(Sums& s, uint32_t c0, uint32_t c1) {
+    uint32_t v[2][16];
+    tmem_load16(c0, v[0]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]), v[16 + i] = __uint_as_float(b[i]);
+    for (int c = 0; c < 8; ++c) {
+        tmem_wait_load(v[c & 1]);
+        if (c + 1 < 8) tmem_load16((c + 1 < 4 ? c0 : c1) + ((c + 1) & 3) * 16, v[(c + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t pair = pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]);
+            s.v[8 * c + i] = FIRST ? pair : add2(s.v[8 * c + i], pair);
+        }
+    }
 }
 
 // A warp's box on its way out: 32 rows of 128 bytes in shared memory, 16-byte
@@ -137,15 +167,6 @@ struct Box {
     }
 };
 
-// 32 values as bf16 into four chunks of a box.
-__device__ __forceinline__ void put_bf16(const Box& box, int chunk, const float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        box.put(chunk + i,
-                make_uint4(pack_bf16x2_rn(v[8 * i], v[8 * i + 1]), pack_bf16x2_rn(v[8 * i + 2], v[8 * i + 3]),
-                           pack_bf16x2_rn(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2_rn(v[8 * i + 6], v[8 * i + 7])));
-}
-
 // Four E4M3 codes.
 __device__ __forceinline__ float4 unpack_e4m3(uint32_t w) {
     uint32_t lo, hi;
@@ -157,102 +178,125 @@ __device__ __forceinline__ float4 unpack_e4m3(uint32_t w) {
     return f;
 }
 
-// up: h from the gate columns (accumulator columns 0 ..) and the up columns (128 ..),
-// 64 of them by each half of the warps; then the codes, of g by one half and of u by
-// the other, so that a lane holds a whole group of its row.
+// up: a lane has 64 gate and the same 64 up columns of its row; the other 64 are
+// with the warp of the other half, and so the groups' maxima are exchanged.  The
+// codes of a row's 128 gate columns leave from one warp's box, those of its up
+// columns from the other's.
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
-                                          const Box& box, uint32_t acc, int half, int n, int row, int rows) {
+                                          const Box& box, unsigned char* other, float (*maxima)[2][kTileM], const Sums& s,
+                                          int quarter, int half, int n, int row, int rows) {
     box.begin();
+    float top_g = 0.0f, top_u = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float g[32], u[32];
-        tmem_load32(acc + half * 64 + c * 32, g);
-        tmem_load32(acc + kGroup + half * 64 + c * 32, u);
+    for (int c = 0; c < 8; ++c) {
+        uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) g[i] = gated(g[i], u[i]);
-        put_bf16(box, 4 * c, g);
+        for (int i = 0; i < 4; ++i) {
+            const float2 g = s.at(4 * c + i), u = s.at(32 + 4 * c + i);
+            h[i] = pack_bf16x2_rn(gated(g.x, u.x), gated(g.y, u.y));
+            top_g = fmaxf(top_g, fmaxf(fabsf(g.x), fabsf(g.y)));
+            top_u = fmaxf(top_u, fmaxf(fabsf(u.x), fabsf(u.y)));
+        }
+        box.put(c, make_uint4(h[0], h[1], h[2], h[3]));
     }
     const int x = n * kGroup + half * 64;
     box.send(map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
     if (pr.codes == nullptr) return;
-    acc += half * kGroup;
-    float amax = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_load32(acc + c * 32, v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    }
-    // a tiny group is scaled up first, so that 448 / amax stays finite
-    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
-    const float inv = amax > 0.0f ? kE4M3Max / (amax * lift) : 0.0f;
+    const int in_tile = quarter * 32 + box.lane;
+    maxima[half][0][in_tile] = top_g;
+    maxima[half][1][in_tile] = top_u;
     box.begin();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both maxima, both boxes free
+    top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
+    top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float v[32];
-        tmem_load32(acc + c * 32, v);
-        uint32_t q[8];
+    for (int m = 0; m < 2; ++m) {
+        const float top = m == 0 ? top_g : top_u;
+        // a tiny group is scaled up first, so that 448 / top stays finite
+        const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
+        const float inv = top > 0.0f ? kE4M3Max / (top * lift) : 0.0f;
+        const Box to = {half == m ? box.staging : other, box.lane};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[i] = pack_e4m3x2(v[4 * i] * lift * inv, v[4 * i + 1] * lift * inv) |
-                   pack_e4m3x2(v[4 * i + 2] * lift * inv, v[4 * i + 3] * lift * inv) << 16;
-        box.put(2 * c, make_uint4(q[0], q[1], q[2], q[3]));
-        box.put(2 * c + 1, make_uint4(q[4], q[5], q[6], q[7]));
+        for (int c = 0; c < 4; ++c) {
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = s.at(32 * m + 8 * c + 2 * i), b = s.at(32 * m + 8 * c + 2 * i + 1);
+                q[i] = pack_e4m3x2(a.x * lift * inv, a.y * lift * inv) | pack_e4m3x2(b.x * lift * inv, b.y * lift * inv) << 16;
+            }
+            to.put(half * 4 + c, make_uint4(q[0], q[1], q[2], q[3]));
+        }
     }
+    fence_async_shared();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
     const int xc = half * pr.N + n * kGroup;
     box.send(map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
     if (box.lane < rows)
-        pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] = amax / kE4M3Max;
+        pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] =
+            (half == 0 ? top_g : top_u) / kE4M3Max;
 }
 
-// down, up_back, and grad in bf16: 128 columns of each half of the warps.
-__device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Box& box, uint32_t acc, int x, int row, int rows,
+// down, up_back, and grad in bf16.
+__device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Box& box, const Sums& s, int x, int row, int rows,
                                             uint16_t* out, int width) {
-#pragma unroll 1
+#pragma unroll
     for (int b = 0; b < 2; ++b) {
         box.begin();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float v[32];
-            tmem_load32(acc + b * 64 + c * 32, v);
-            put_bf16(box, 4 * c, v);
+        for (int c = 0; c < 8; ++c) {
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = s.at(32 * b + 4 * c + i);
+                q[i] = pack_bf16x2_rn(v.x, v.y);
+            }
+            box.put(c, make_uint4(q[0], q[1], q[2], q[3]));
         }
         box.send(map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
     }
 }
 
+// 16 bytes of a line that this lane reads on (L1 keeps the rest of its sector).
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
 // down_back: a lane has one 128-group of its row, whose scales and sum are its own.
 __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtensorMap* map_hg, const CUtensorMap* map_dgu,
-                                                 const Box& box, uint32_t acc, int blk, int row, int rows) {
+                                                 const Box& box, Sums& d, int blk, int row, int rows) {
     const size_t mine = (size_t)row + max(0, min(box.lane, rows - 1));
     const int groups = pr.N / kGroup;
     const float gate = __ldg(pr.row_gates + mine);
     const float sg = __ldg(pr.scales + mine * pr.scale_stride + blk);
     const float su = __ldg(pr.scales + mine * pr.scale_stride + groups + blk);
     const uint8_t* codes = pr.codes + mine * 2 * pr.N + blk * kGroup;
+    uint4 next_g = ld_once16(codes), next_u = ld_once16(codes + pr.N);
     float sum = 0.0f;
+    // One half after the other, the second moved to where the first was: unrolled,
+    // this takes more registers than there are.
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
         uint32_t du[32], hg[32];  // bf16 pairs of 64 columns
         box.begin();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 16 columns
-            const uint4 cg = __ldg(reinterpret_cast<const uint4*>(codes + b * 64 + c * 16));
-            const uint4 cu = __ldg(reinterpret_cast<const uint4*>(codes + pr.N + b * 64 + c * 16));
-            uint32_t d[16];
-            tmem_load16(acc + b * 64 + c * 16, d);
-            tmem_wait_load(d);
+            const uint4 cg = next_g, cu = next_u;
+            const int next = b * 64 + c * 16 + 16;  // a step ahead, and no further: registers
+            if (next < kGroup) next_g = ld_once16(codes + next), next_u = ld_once16(codes + pr.N + next);
             const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
             uint32_t dg[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 fg = unpack_e4m3(wg[q]), fu = unpack_e4m3(wu[q]);
                 const float gs[4] = {fg.x, fg.y, fg.z, fg.w}, us[4] = {fu.x, fu.y, fu.z, fu.w};
+                const float2 d0 = d.at(8 * c + 2 * q), d1 = d.at(8 * c + 2 * q + 1);
+                const float ds[4] = {d0.x, d0.y, d1.x, d1.y};
                 float vg[4], vu[4], vh[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float g = gs[i] * sg, u = us[i] * su, dd = __uint_as_float(d[4 * q + i]);
+                    const float g = gs[i] * sg, u = us[i] * su, dd = ds[i];
                     const float s = sigmoid(g), silu = g * s, h = silu * u, dh = gate * dd;
                     sum += dd * h;
                     vg[i] = dh * u * (s * (1.0f + g * (1.0f - s)));
@@ -277,21 +321,22 @@ __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtens
 #pragma unroll
         for (int c = 0; c < 8; ++c) box.put(c, make_uint4(hg[4 * c], hg[4 * c + 1], hg[4 * c + 2], hg[4 * c + 3]));
         box.send(map_hg, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d.v[i] = d.v[32 + i];
     }
     if (box.lane < rows) pr.parts[mine * groups + blk] = sum;
 }
 
-// grad in fp32: 128 columns of each half of the warps, four boxes of 32.
-__device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Box& box, uint32_t acc, int x, int row, bool add) {
-#pragma unroll 1
+// grad in fp32: four boxes of 32 columns.
+__device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Box& box, const Sums& s, int x, int row, bool add) {
+#pragma unroll
     for (int b = 0; b < 4; ++b) {
         box.begin();
-        float v[32];
-        tmem_load32(acc + b * 32, v);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            box.put(c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                                  __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3])));
+        for (int c = 0; c < 8; ++c) {
+            const float2 u = s.at(16 * b + 2 * c), v = s.at(16 * b + 2 * c + 1);
+            box.put(c, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y)));
+        }
         fence_async_shared();
         __syncwarp();
         if (elect_one()) {
@@ -311,6 +356,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
              const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
+    constexpr int kChunk = chunk_of(OP);
     extern __shared__ __align__(1024) unsigned char smem[];
     const int stages = pr.stages;
     // The kernel has no other shared memory, so the base lies on a 1024-byte
@@ -372,6 +418,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     // of zeros (past the end of the rows), so that its gradient is zeros like any other's.
     const auto steps_of = [&](const int4& t) { return kGrad ? max(1, (t.w + kStepK - 1) / kStepK) : pr.K / kStepK; };
 
+    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
         if (elect_one()) {
             int s = 0;
@@ -448,55 +495,59 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const uint64_t desc_b = kBMn ? umma_desc_mn(smem + kABytes, kBlockBytes) : umma_desc(smem + kABytes);
         // From one 16 of the inner dimension to the next: 32 bytes along a row, or 16 rows.
         constexpr uint32_t kNextA = kGrad ? 16 * kLine / 16 : 2, kNextB = kBMn ? 16 * kLine / 16 : 2;
-        uint32_t j = 0, done = 0;  // tiles and steps of this CTA
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+        uint32_t j = 0, done = 0, unit = 0;  // tiles, steps and chunks of this CTA
+        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
             if (!(ok = __all_sync(kFull, tile_written(j)))) break;
             const int4 t = tile_at(j);
             const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
             const uint32_t idesc = umma_idesc_bf16(kTileM, two ? kTileN : kGroup, kGrad, kBMn);
-            const uint32_t buf = j & 1, d = tmem + buf * kTileN;
             const int steps = steps_of(t), whole = kGrad ? t.w / kStepK : steps;
-            if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_empty[buf], ((j >> 1) & 1) ^ 1, gave_up)))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                uint32_t s = done % stages, phase = (done / stages) & 1;
-                for (int k = 0; k < whole; ++k) {
-                    if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
-                    tc_fence_after();
-                    const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
-#pragma unroll
-                    for (int i = 0; i < kStepK / 16; ++i)
-                        umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > 0 || i > 0);
-                    umma_commit(&b.empty[s]);
-                    if (++s == stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
-                if (ok && whole == steps) umma_commit(&b.acc_full[buf]);
-            }
-            if (!(ok = __all_sync(kFull, ok))) break;
-            if (kGrad && whole < steps) {
-                // The window's last rows: cleared behind them up to a multiple of 16.
-                const uint32_t last = done + whole, s = last % stages, phase = (last / stages) & 1;
-                if (!(ok = __all_sync(kFull, mbar_wait(&b.full[s], phase, gave_up)))) break;
-                const int valid = t.w - whole * kStepK, up = max(16, (valid + 15) & ~15);
-                const int chunks = (up - valid) * 8;
-                for (int i = lane; valid > 0 && i < (two ? 6 : 4) * chunks; i += 32) {  // 64-element blocks of A, then of B
-                    const int blk = i / chunks, at = i - blk * chunks;
-                    st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
-                }
-                fence_async_shared();
-                __syncwarp();
+            for (int k0 = 0; k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
+                const uint32_t buf = unit & 1, d = tmem + buf * kTileN;
+                const int end = k0 + min(kChunk, steps - k0), whole_end = min(end, whole);
+                if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_empty[buf], ((unit >> 1) & 1) ^ 1, gave_up)))) break;
+                tc_fence_after();
                 if (elect_one()) {
-                    tc_fence_after();
-                    const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
-                    for (int i = 0; i < up / 16; ++i)
-                        umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, whole > 0 || i > 0);
-                    umma_commit(&b.empty[s]);
-                    umma_commit(&b.acc_full[buf]);
+                    uint32_t s = (done + k0) % stages, phase = ((done + k0) / stages) & 1;
+                    for (int k = k0; k < whole_end; ++k) {
+                        if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
+                        tc_fence_after();
+                        const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
+#pragma unroll
+                        for (int i = 0; i < kStepK / 16; ++i)
+                            umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                        umma_commit(&b.empty[s]);
+                        if (++s == stages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok && whole_end == end) umma_commit(&b.acc_full[buf]);
                 }
-                __syncwarp();
+                if (!(ok = __all_sync(kFull, ok))) break;
+                if (kGrad && whole_end < end) {
+                    // The window's last rows: cleared behind them up to a multiple of 16.
+                    const uint32_t last = done + whole, s = last % stages, phase = (last / stages) & 1;
+                    if (!(ok = __all_sync(kFull, mbar_wait(&b.full[s], phase, gave_up)))) break;
+                    const int valid = t.w - whole * kStepK, up = max(16, (valid + 15) & ~15);
+                    const int chunks = (up - valid) * 8;
+                    // 64-element blocks of A, then of B; the rows of an empty window are zeros already
+                    for (int i = lane; valid > 0 && i < (two ? 6 : 4) * chunks; i += 32) {
+                        const int blk = i / chunks, at = i - blk * chunks;
+                        st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (elect_one()) {
+                        tc_fence_after();
+                        const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
+                        for (int i = 0; i < up / 16; ++i)
+                            umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, whole_end > k0 || i > 0);
+                        umma_commit(&b.empty[s]);
+                        umma_commit(&b.acc_full[buf]);
+                    }
+                    __syncwarp();
+                }
             }
             done += steps;
         }
@@ -507,38 +558,53 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
             }
         }
-    } else {
+    } else if (warp < kSumWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // Finishing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
         // lane) and one half of the tile's columns.
         const int quarter = warp & 3, half = warp >> 2;
         const Box box = {staging + warp * kStaging, lane};
-        uint32_t j = 0;
-        for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
-            if (!__all_sync(kFull, tile_written(j))) break;
+        const uint32_t c0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (OP == Op::kUp ? 64 : kGroup);
+        const uint32_t c1 = c0 + (OP == Op::kUp ? kGroup : 64);
+        uint32_t j = 0, unit = 0;
+        bool ok = true;
+        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
+            if (!(ok = __all_sync(kFull, tile_written(j)))) break;
             const int4 t = tile_at(j);
-            const uint32_t buf = j & 1;
-            if (!__all_sync(kFull, mbar_wait(&b.acc_full[buf], (j >> 1) & 1, gave_up))) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTileN;
             const int row = (kGrad ? t.x : t.z) + quarter * 32;
             const int rows = kGrad ? kRowBox : max(0, min(kRowBox, t.w - quarter * 32));
             const int blk = 2 * t.y + half;  // this half's 128 columns (up: of another kind)
-            if constexpr (OP == Op::kUp) {
-                if (rows > 0) finish_up(pr, &map_out, &map_out2, box, acc, half, t.y, row, rows);
-            } else if (rows > 0 && blk < blocks) {
-                const uint32_t mine = acc + half * kGroup;
-                if constexpr (OP == Op::kDownBack)
-                    finish_down_back(pr, &map_out, &map_out2, box, mine, blk, row, rows);
-                else if constexpr (!kGrad)
-                    finish_rows(&map_out, box, mine, blk * kGroup, row, rows, pr.out, pr.N);
-                else if (pr.grad == MOE_GRAD_BF16)
-                    finish_rows(&map_out, box, mine, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
-                else if (pr.grad == MOE_GRAD_F32 || t.w > 0)
-                    finish_grad(&map_out, box, mine, blk * kGroup, row, pr.grad == MOE_GRAD_F32_ADD);
+            const bool busy = rows > 0 && (OP == Op::kUp || blk < blocks);
+            const int steps = steps_of(t);
+            Sums s;
+            for (int k0 = 0; k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
+                const uint32_t buf = unit & 1;
+                if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_full[buf], (unit >> 1) & 1, gave_up)))) break;
+                tc_fence_after();
+                if (busy) {
+                    if (k0 == 0)
+                        take_sums<true>(s, c0 + buf * kTileN, c1 + buf * kTileN);
+                    else
+                        take_sums<false>(s, c0 + buf * kTileN, c1 + buf * kTileN);
+                }
+                // the accumulator is read: it may be written again
+                tc_fence_before();
+                __syncwarp();
+                if (elect_one()) mbar_arrive(&b.acc_empty[buf]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (elect_one()) mbar_arrive(&b.acc_empty[buf]);
+            if (!ok) break;
+            if (!busy) continue;
+            if constexpr (OP == Op::kUp)
+                finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kStaging, b.maxima, s, quarter, half, t.y, row,
+                          rows);
+            else if constexpr (OP == Op::kDownBack)
+                finish_down_back(pr, &map_out, &map_out2, box, s, blk, row, rows);
+            else if constexpr (!kGrad)
+                finish_rows(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
+            else if (pr.grad == MOE_GRAD_BF16)
+                finish_rows(&map_out, box, s, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
+            else if (pr.grad == MOE_GRAD_F32 || t.w > 0)
+                finish_grad(&map_out, box, s, blk * kGroup, row, pr.grad == MOE_GRAD_F32_ADD);
         }
         if (elect_one()) bulk_wait();
         __syncwarp();
