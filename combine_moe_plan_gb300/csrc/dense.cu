@@ -7,16 +7,19 @@
 //   up_back    dx = dgu w13
 //   grad       dw = a^T b over the rows of a window
 //
-// Mapping.  One persistent CTA per SM walks tiles of 128 by 256 outputs.  One
-// thread loads operands by TMA (64 inner elements a stage), one issues
-// tcgen05.mma (128 x 256 x 16) into one of two TMEM accumulators, eight warps
-// finish the tile in the other: they read it, do what the product ends in, and
-// send it out by TMA, each warp its own 32 rows in boxes of 128 bytes.
+// Mapping.  Pairs of CTAs (clusters of two, one CTA per SM) walk tiles of 256 by
+// 256 outputs, 128 rows in each CTA.  In each, one thread loads its half of both
+// operands by TMA (64 inner elements a stage); one thread of the first CTA issues
+// tcgen05.mma for both (256 x 256 x 16) into one of two TMEM accumulators; eight
+// warps read the other accumulator, do what the product ends in, and send it out by
+// TMA, each warp its own 32 rows in boxes of 128 bytes.  A CTA by itself (128 x 256)
+// has to fetch 48 KB for 512 cycles of products, and an SM gets 64 bytes a cycle
+// from L2: 768 cycles.  A pair fetches 32 KB a CTA.
 //   Rows are the M operand of every product with weights.  Weights are read as
 // they lie: where the product runs over a row's inputs (up, down) they are a
 // K-major operand, where it runs over the outputs (down_back, up_back) an MN-major
 // one, and for grad both operands are: a window's rows are the inner dimension, of
-// any number.  There the last stage's rows past the window are cleared in shared
+// any number.  There a warp clears the last stage's rows past the window in shared
 // memory up to the next multiple of 16 (another expert's rows, or none: a NaN
 // there must not meet a zero), and the rest are left out.
 #include <cuda.h>
@@ -32,20 +35,21 @@ namespace moe {
 namespace {
 
 constexpr int kMostExperts = 4096;
-constexpr int kTileM = 128, kTileN = 256, kStepK = 64;
+constexpr int kTileM = 256, kTileN = 256, kStepK = 64;
+constexpr int kHalfM = kTileM / 2;                // a CTA's rows (TMEM lanes)
 constexpr int kRowBox = 32;                       // rows per TMA box of a row operand and of an output
 constexpr int kLine = 128;                        // bytes of a box's row
-constexpr int kABytes = kTileM * kLine;
-constexpr int kStageBytes = kABytes + kTileN * kLine;
-constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an MN-major operand
+constexpr int kABytes = kHalfM * kLine;
+constexpr int kStageBytes = kABytes + kTileN / 2 * kLine;
+constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an operand
 constexpr int kSumWarps = 8;                      // warps that finish tiles
-constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
+constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kClearWarp = kSumWarps + 2;
 constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
 // 256 x 216 + 128 x 72 = 64,512.
 constexpr int kSumRegs = 216, kOtherRegs = 72;
 constexpr int kStaging = kRowBox * kLine;         // of one warp
-constexpr int kMostStages = 4;
+constexpr int kMostStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
 
 // The loading thread looks each tile up and leaves it in a ring for the other
@@ -64,22 +68,23 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 __host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 4; }
 
 struct alignas(16) Barriers {
-    uint64_t full[kMostStages], empty[kMostStages];  // stages
-    uint64_t acc_full[2], acc_empty[2];              // accumulators
+    uint64_t full[kMostStages], empty[kMostStages];  // stages; full: both CTAs', in the first
+    uint64_t landed[kMostStages];                    // grad: this CTA's half of a stage to be cleared
+    uint64_t acc_full[2], acc_empty[2];              // accumulators; empty: both CTAs', in the first
     uint64_t known[kTileRing];                       // tiles[i] is written
-    uint64_t drain;
-    // up .. up_back: expert, n, row, valid; grad: first row of dw, n, first row of the window, rows in it
+    // up .. up_back: expert, n, and of this CTA's half the first row and how many are valid;
+    // grad: first row of this CTA's half in dw (-1: none), n, first row of the window, rows in it
     int4 tiles[kTileRing];
     uint32_t tmem;
     int gave_up;
     int warp_total[kDenseThreads / 32], warp_top[kDenseThreads / 32];
-    float maxima[2][2][kTileM];  // up: of gate and up columns, of the two halves of each row
+    float maxima[2][2][kHalfM];  // up: of gate and up columns, of the two halves of each row
 };
 
 __host__ __device__ constexpr size_t smem_bytes(int stages, int P) {
     return (size_t)stages * kStageBytes + kSumWarps * kStaging + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
 }
-static_assert(smem_bytes(3, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
+static_assert(smem_bytes(kMostStages - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
 
 struct Problem {
     int P, N, K;  // experts, outputs a row, inner size; grad: columns of b and of a
@@ -183,7 +188,7 @@ __device__ __forceinline__ float4 unpack_e4m3(uint32_t w) {
 // codes of a row's 128 gate columns leave from one warp's box, those of its up
 // columns from the other's.
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
-                                          const Box& box, unsigned char* other, float (*maxima)[2][kTileM], const Sums& s,
+                                          const Box& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
                                           int quarter, int half, int n, int row, int rows) {
     box.begin();
     float top_g = 0.0f, top_u = 0.0f;
@@ -352,8 +357,8 @@ __device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Box& b
 
 template <Op OP>
 __global__ void __launch_bounds__(kDenseThreads, 1)
-dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
+dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a_small,
+             const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
     constexpr int kChunk = chunk_of(OP);
@@ -372,42 +377,47 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     volatile int* gave_up = &b.gave_up;
     // Uniform in a warp, and through the shuffle known to be.
     const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int s = 0; s < stages; ++s) {
-                mbar_init(&b.full[s], 1);
+                mbar_init(&b.full[s], 2);
                 mbar_init(&b.empty[s], 1);
+                mbar_init(&b.landed[s], 1);
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&b.acc_full[s], 1);
-                mbar_init(&b.acc_empty[s], kSumWarps);
+                mbar_init(&b.acc_empty[s], 2 * kSumWarps);
             }
             for (int i = 0; i < kTileRing; ++i) mbar_init(&b.known[i], 1);
-            mbar_init(&b.drain, 1);
             b.gave_up = 0;
             mbar_init_fence();
         }
         __syncwarp();
-        tmem_alloc_all(&b.tmem);
+        tmem_alloc_all_pair(&b.tmem);
         tc_fence_before();
     } else if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_a_small);
         tma_prefetch_map(&map_b);
         tma_prefetch_map(&map_out);
         tma_prefetch_map(&map_out2);
     }
+    cluster_arrive();
     grid_dependency_sync();
     allow_dependents();
     const int blocks = pr.N / kGroup;  // 128-blocks of outputs
     const int n_tiles = OP == Op::kUp ? blocks : (blocks + 1) / 2;
-    // its barriers publish the above
+    // its barriers publish the above to this CTA, the cluster's to the other
     const int m_total = scan_windows<kDenseThreads, kGrad ? kStepK : kTileM>(
-        pr.offsets, pr.P, pr.rows, pr.err, kGrad ? 1 : n_tiles, first_m, b.warp_total, b.warp_top, &b.tiles[0]);
+        pr.offsets, pr.P, pr.rows, pr.err, first_m, b.warp_total, b.warp_top);
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
     // at most 2^31: checked by the host
-    const long long tiles = (long long)(kGrad ? pr.P * (pr.K / kTileM) : m_total) * n_tiles;
+    const int m_tiles = (pr.K + kTileM - 1) / kTileM;  // grad
+    const long long tiles = (long long)(kGrad ? pr.P * m_tiles : m_total) * n_tiles;
 
     // Tile number j of this CTA, once the loading thread has left it in the ring.
     const auto tile_written = [&](uint32_t j) {
@@ -425,54 +435,55 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             uint32_t phase = 0, issued = 0;
             bool ok = true;
             TileWalk<kTileM> walk;
+            const uint32_t full = peer_smem(smem_u32(&b.full[0]), 0);
             uint32_t j = 0;
-            for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++j) {
+            for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
                 // no tile is written any more, so none overwrites one that a
                 // warp which runs on without waiting is reading
                 if (!(ok = ok && *gave_up == 0)) break;
                 int4 t;
-                int b_row = 0, m0 = 0;
+                int m0 = 0, p;
                 if constexpr (kGrad) {
-                    const int m_tiles = pr.K / kTileM, mn = (int)tile / n_tiles, p = mn / m_tiles;
-                    m0 = (mn - p * m_tiles) * kTileM;
+                    const int mn = (int)(tile / n_tiles);
+                    p = mn / m_tiles;
+                    m0 = (mn - p * m_tiles) * kTileM + rank * kHalfM;
                     const int lo = pr.offsets[p], count = first_m[p + 1] > first_m[p] ? pr.offsets[p + 1] - lo : 0;
-                    t = make_int4(p * pr.K + m0, (int)tile - mn * n_tiles, count > 0 ? lo : pr.rows, count);
+                    t = make_int4(m0 < pr.K ? p * pr.K + m0 : -1, (int)(tile - (long long)mn * n_tiles),
+                                  count > 0 ? lo : pr.rows, count);
                 } else {
-                    if (j == 0) {
-                        t = b.tiles[0];
-                        walk.p = t.x;
-                    } else {
-                        const Tile w = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
-                        t = make_int4(w.p, w.n, w.row, w.valid);
-                    }
-                    b_row = kBMn ? t.x * pr.K : t.x * (OP == Op::kUp ? 2 : 1) * pr.N + t.y * (OP == Op::kUp ? kGroup : kTileN);
+                    const Tile w = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
+                    p = w.p;
+                    t = make_int4(p, w.n, w.row + rank * kHalfM, max(0, min(kHalfM, w.valid - rank * kHalfM)));
                 }
-                if (kGrad || j > 0) b.tiles[j % kTileRing] = t;
+                b.tiles[j % kTileRing] = t;
                 mbar_arrive(&b.known[j % kTileRing]);
                 const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
                 const int steps = steps_of(t);
-                const int boxes = kGrad ? kTileM / kStepK : (t.w + kRowBox - 1) / kRowBox;
-                const uint32_t bytes = (kGrad ? kABytes : boxes * kStaging) + (two ? 2 : 1) * kGroup * kLine;
+                // This CTA's half of the tile's columns begins at n0.  128 are loaded;
+                // with one block of 128 outputs left the pair takes 64 of each.
+                const int n0 = OP == Op::kUp ? t.y * kGroup + rank * pr.N : t.y * kTileN + rank * (two ? kGroup : 64);
+                // A whole box of rows, or as many small ones as hold any: a few
+                // rows an expert should not cost 16 KB a stage.
+                const int small = !kGrad && t.w <= 64 ? (t.w + kRowBox - 1) / kRowBox : 0;
+                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kStaging : 0);
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
                     unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
-                    uint64_t* bar = &b.full[s];
-                    mbar_expect_tx(bar, bytes);
-                    if constexpr (kBMn) {
-                        const int y = kGrad ? t.z + k * kStepK : b_row + k * kStepK;
-                        for (int i = 0; i < (two ? 4 : 2); ++i)
-                            tma_load_2d(pb + i * kBlockBytes, &map_b, t.y * kTileN + i * kStepK, y, bar);
-                    } else {
-                        tma_load_2d(pb, &map_b, k * kStepK, b_row, bar);
-                        if (two)
-                            tma_load_2d(pb + kGroup * kLine, &map_b, k * kStepK, b_row + (OP == Op::kUp ? pr.N : kGroup), bar);
-                    }
+                    uint32_t bar = full + 8 * s;
+                    if (kGrad && t.w > 0 && (k + 1) * kStepK > t.w) bar = peer_smem(smem_u32(&b.landed[s]), rank);
+                    mbar_expect_tx_cluster(bar, bytes);
+                    const int inner = k * kStepK;
+                    if constexpr (kBMn)
+                        tma_load_3d_pair(pb, &map_b, 0, (kGrad ? t.z : p * pr.K) + inner, n0 / 64, bar);
+                    else
+                        tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
                     if constexpr (kGrad) {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(pa + i * kBlockBytes, &map_a, m0 + i * kStepK, t.z + k * kStepK, bar);
+                        tma_load_3d_pair(pa, &map_a, 0, t.z + inner, m0 / 64, bar);
+                    } else if (t.w > 64) {
+                        tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
                     } else {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(pa + i * kStaging, &map_a, k * kStepK, t.z + i * kRowBox, bar);
+                        for (int i = 0; i < small; ++i)
+                            tma_load_2d_pair(pa + i * kStaging, &map_a_small, inner, t.z + i * kRowBox, bar);
                     }
                     ++issued;
                     if (++s == stages) {
@@ -482,82 +493,78 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             }
             if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
-            // Leave only after the copies in flight have landed (or never will),
-            // also where this thread was through before another wait gave up.
+            // Leave only after the copies in flight have landed and been read (or
+            // never will), also where this thread was through before another wait gave up.
             const uint64_t t0 = now_ns();
             for (uint32_t i = issued > (uint32_t)stages ? issued - stages : 0; i < issued; ++i)
-                while (!mbar_try(smem_u32(&b.full[i % stages]), (i / stages) & 1) && now_ns() - t0 < kStallNs) {
+                while (!mbar_try(smem_u32(&b.empty[i % stages]), (i / stages) & 1) && now_ns() - t0 < kStallNs) {
                 }
         }
     } else if (warp == kMmaWarp) {
-        bool ok = true;
-        const uint64_t desc_a = kGrad ? umma_desc_mn(smem, kBlockBytes) : umma_desc(smem);
-        const uint64_t desc_b = kBMn ? umma_desc_mn(smem + kABytes, kBlockBytes) : umma_desc(smem + kABytes);
-        // From one 16 of the inner dimension to the next: 32 bytes along a row, or 16 rows.
-        constexpr uint32_t kNextA = kGrad ? 16 * kLine / 16 : 2, kNextB = kBMn ? 16 * kLine / 16 : 2;
-        uint32_t j = 0, done = 0, unit = 0;  // tiles, steps and chunks of this CTA
-        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
-            if (!(ok = __all_sync(kFull, tile_written(j)))) break;
-            const int4 t = tile_at(j);
-            const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
-            const uint32_t idesc = umma_idesc_bf16(kTileM, two ? kTileN : kGroup, kGrad, kBMn);
-            const int steps = steps_of(t), whole = kGrad ? t.w / kStepK : steps;
-            for (int k0 = 0; k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
-                const uint32_t buf = unit & 1, d = tmem + buf * kTileN;
-                const int end = k0 + min(kChunk, steps - k0), whole_end = min(end, whole);
-                if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_empty[buf], ((unit >> 1) & 1) ^ 1, gave_up)))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    uint32_t s = (done + k0) % stages, phase = ((done + k0) / stages) & 1;
-                    for (int k = k0; k < whole_end; ++k) {
+        if (rank == 0 && elect_one()) {
+            bool ok = true;
+            const uint64_t desc_a = kGrad ? umma_desc_mn(smem, kBlockBytes) : umma_desc(smem);
+            const uint64_t desc_b = kBMn ? umma_desc_mn(smem + kABytes, kBlockBytes) : umma_desc(smem + kABytes);
+            // From one 16 of the inner dimension to the next: 32 bytes along a row, or 16 rows.
+            constexpr uint32_t kNextA = kGrad ? 16 * kLine / 16 : 2, kNextB = kBMn ? 16 * kLine / 16 : 2;
+            int s = 0;
+            uint32_t phase = 0, j = 0, unit = 0;  // tiles and chunks of this pair
+            for (long long tile = pair; ok && tile < tiles; tile += pairs, ++j) {
+                if (!(ok = tile_written(j))) break;
+                const int4 t = tile_at(j);
+                const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
+                const uint32_t idesc = umma_idesc_bf16(kTileM, two ? kTileN : kGroup, kGrad, kBMn);
+                const int steps = steps_of(t);
+                for (int k0 = 0; ok && k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
+                    const uint32_t buf = unit & 1, d = tmem + buf * kTileN;
+                    const int end = k0 + min(kChunk, steps - k0);
+                    if (!(ok = mbar_wait_pair(&b.acc_empty[buf], ((unit >> 1) & 1) ^ 1, gave_up))) break;
+                    for (int k = k0; k < end; ++k) {
                         if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
+                        // cleared rows of the other CTA
+                        if (kGrad && (k + 1) * kStepK > t.w) (void)mbar_wait_pair(&b.full[s], phase, gave_up);
                         tc_fence_after();
-                        const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
+                        const uint64_t da = desc_a + (uint32_t)s * (kStageBytes / 16);
+                        const uint64_t db = desc_b + (uint32_t)s * (kStageBytes / 16);
+                        // the window's last rows: no more than hold any
+                        const int parts = kGrad ? max(1, min(kStepK / 16, (t.w - k * kStepK + 15) >> 4)) : kStepK / 16;
 #pragma unroll
                         for (int i = 0; i < kStepK / 16; ++i)
-                            umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
-                        umma_commit(&b.empty[s]);
+                            if (i < parts) umma_bf16_pair(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                        umma_commit_pair(&b.empty[s]);
                         if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
                     }
-                    if (ok && whole_end == end) umma_commit(&b.acc_full[buf]);
-                }
-                if (!(ok = __all_sync(kFull, ok))) break;
-                if (kGrad && whole_end < end) {
-                    // The window's last rows: cleared behind them up to a multiple of 16.
-                    const uint32_t last = done + whole, s = last % stages, phase = (last / stages) & 1;
-                    if (!(ok = __all_sync(kFull, mbar_wait(&b.full[s], phase, gave_up)))) break;
-                    const int valid = t.w - whole * kStepK, up = max(16, (valid + 15) & ~15);
-                    const int chunks = (up - valid) * 8;
-                    // 64-element blocks of A, then of B; the rows of an empty window are zeros already
-                    for (int i = lane; valid > 0 && i < (two ? 6 : 4) * chunks; i += 32) {
-                        const int blk = i / chunks, at = i - blk * chunks;
-                        st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
-                    }
-                    fence_async_shared();
-                    __syncwarp();
-                    if (elect_one()) {
-                        tc_fence_after();
-                        const uint64_t da = desc_a + s * (kStageBytes / 16), db = desc_b + s * (kStageBytes / 16);
-                        for (int i = 0; i < up / 16; ++i)
-                            umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, whole_end > k0 || i > 0);
-                        umma_commit(&b.empty[s]);
-                        umma_commit(&b.acc_full[buf]);
-                    }
-                    __syncwarp();
+                    if (ok) umma_commit_pair(&b.acc_full[buf]);
                 }
             }
-            done += steps;
-        }
-        if (elect_one()) {
             if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
-            umma_commit(&b.drain);  // leave only after the products in flight
-            const uint64_t t0 = now_ns();
-            while (!mbar_try(smem_u32(&b.drain), 0) && now_ns() - t0 < kStallNs) {
-            }
         }
+    } else if (kGrad && warp == kClearWarp) {
+        // The rows past a window in its last stage, cleared up to a multiple of 16.
+        uint32_t j = 0, done = 0, phases = 0;  // steps; a bit a stage
+        for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
+            if (!__all_sync(kFull, tile_written(j))) break;
+            const int4 t = tile_at(j);
+            const int valid = t.w % kStepK;
+            if (valid > 0) {
+                const uint32_t s = (done + t.w / kStepK) % stages;
+                if (!__all_sync(kFull, mbar_wait(&b.landed[s], (phases >> s) & 1, gave_up))) break;
+                phases ^= 1u << s;
+                const int chunks = (((valid + 15) & ~15) - valid) * 8, b_blocks = 2 * t.y + 1 < blocks ? 2 : 1;
+                for (int i = lane; i < (2 + b_blocks) * chunks; i += 32) {  // 64-blocks of A, then of B
+                    const int blk = i / chunks, at = i - blk * chunks;
+                    st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (elect_one()) mbar_arrive_cluster(peer_smem(smem_u32(&b.full[s]), 0));
+            }
+            done += steps_of(t);
+        }
+        if (*gave_up && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
     } else if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // Finishing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
@@ -566,13 +573,14 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const Box box = {staging + warp * kStaging, lane};
         const uint32_t c0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (OP == Op::kUp ? 64 : kGroup);
         const uint32_t c1 = c0 + (OP == Op::kUp ? kGroup : 64);
+        const uint32_t acc_empty = peer_smem(smem_u32(&b.acc_empty[0]), 0);
         uint32_t j = 0, unit = 0;
         bool ok = true;
-        for (long long tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++j) {
+        for (long long tile = pair; ok && tile < tiles; tile += pairs, ++j) {
             if (!(ok = __all_sync(kFull, tile_written(j)))) break;
             const int4 t = tile_at(j);
             const int row = (kGrad ? t.x : t.z) + quarter * 32;
-            const int rows = kGrad ? kRowBox : max(0, min(kRowBox, t.w - quarter * 32));
+            const int rows = kGrad ? (t.x >= 0 ? kRowBox : 0) : max(0, min(kRowBox, t.w - quarter * 32));
             const int blk = 2 * t.y + half;  // this half's 128 columns (up: of another kind)
             const bool busy = rows > 0 && (OP == Op::kUp || blk < blocks);
             const int steps = steps_of(t);
@@ -590,7 +598,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // the accumulator is read: it may be written again
                 tc_fence_before();
                 __syncwarp();
-                if (elect_one()) mbar_arrive(&b.acc_empty[buf]);
+                if (elect_one()) mbar_arrive_cluster(acc_empty + 8 * buf);
             }
             if (!ok) break;
             if (!busy) continue;
@@ -611,11 +619,15 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         if (*gave_up && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
         tc_fence_before();
     }
-    __syncthreads();
+    // Neither CTA leaves while the other may still reach its shared memory or TMEM.
+    // (A hardware barrier of threads whose waits have all ended.)
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
-        tmem_free_all(tmem);
+        tmem_free_all_pair(tmem);
     }
 }
 
@@ -630,14 +642,16 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;
     const int blocks = pr.N / kGroup, n_tiles = OP == Op::kUp ? blocks : (blocks + 1) / 2;
     // The most tiles any windows over these rows can have.
-    const long long m_most = kGrad ? (long long)pr.P * (pr.K / kTileM)
+    const long long m_most = kGrad ? (long long)pr.P * ((pr.K + kTileM - 1) / kTileM)
                                    : ((long long)pr.rows + kTileM - 1) / kTileM + min(pr.P, pr.rows);
     if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
     const size_t rows = (size_t)pr.rows, n_rows = (size_t)pr.P * pr.N, k_rows = (size_t)pr.P * pr.K;
-    CUtensorMap map_a, map_b, map_out, map_out2;
-    bool ok = tile_map(&map_a, kBf16, a, rows, pr.K, kGrad ? kStepK : kRowBox);
-    ok = ok && (kGrad  ? tile_map(&map_b, kBf16, w, rows, pr.N, kStepK)
-                : kBMn ? tile_map(&map_b, kBf16, w, k_rows, pr.N, kStepK)
+    CUtensorMap map_a, map_a_small, map_b, map_out, map_out2;
+    bool ok = kGrad ? block_map(&map_a, a, rows, pr.K, kStepK)
+                    : tile_map(&map_a, kBf16, a, rows, pr.K, kHalfM) && tile_map(&map_a_small, kBf16, a, rows, pr.K, kRowBox);
+    if (kGrad) map_a_small = map_a;
+    ok = ok && (kGrad  ? block_map(&map_b, w, rows, pr.N, kStepK)
+                : kBMn ? block_map(&map_b, w, k_rows, pr.N, kStepK)
                        : tile_map(&map_b, kBf16, w, (OP == Op::kUp ? 2 : 1) * n_rows, pr.K, kGroup));
     if (kGrad)
         ok = ok && tile_map(&map_out, pr.grad == MOE_GRAD_BF16 ? kBf16 : kF32, pr.dw, k_rows, pr.N, kRowBox);
@@ -647,16 +661,16 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
     if (OP == Op::kUp && pr.codes != nullptr) ok = ok && tile_map(&map_out2, kByte, pr.codes, rows, 2 * pr.N, kRowBox);
     if (OP == Op::kDownBack) ok = ok && tile_map(&map_out2, kBf16, pr.dgu, rows, 2 * pr.N, kRowBox);
     if (!ok) return MOE_ERR_CUDA;
-    // Four stages where the prefix of the windows leaves room for them (607 experts and fewer).
+    // Six stages where the prefix of the windows leaves room for them.
     pr.stages = smem_bytes(kMostStages, pr.P) <= kSmemLimit ? kMostStages : kMostStages - 1;
     // The same limit for every size, so that callers on several threads do not lower it for each other.
     if (cudaFuncSetAttribute(dense_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return MOE_ERR_CUDA;
     const int sms = sm_count();
-    if (sms < 1) return MOE_ERR_CUDA;
-    const unsigned grid = (unsigned)(m_most * n_tiles < sms ? m_most * n_tiles : sms);
-    return launch_pdl(dense_kernel<OP>, dim3(grid), dim3(kDenseThreads), smem_bytes(pr.stages, pr.P), s, map_a, map_b,
-                      map_out, map_out2, pr) == cudaSuccess
+    if (sms < 2) return MOE_ERR_CUDA;
+    const unsigned pairs = (unsigned)(m_most * n_tiles < sms / 2 ? m_most * n_tiles : sms / 2);
+    return launch_pdl_cluster(0, 2, dense_kernel<OP>, dim3(2 * pairs), dim3(kDenseThreads), smem_bytes(pr.stages, pr.P), s,
+                              map_a, map_a_small, map_b, map_out, map_out2, pr) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

@@ -181,8 +181,8 @@ experts_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int blocks = pr.N / kGroup;                       // 128-blocks of outputs
     const int n_tiles = UP ? blocks : (blocks + 1) / 2;
     // its barriers publish the above
-    const int m_total = scan_windows<kExpertsThreads, kTileM>(pr.offsets, pr.P, pr.rows, pr.err, n_tiles, first_m,
-                                                              b.warp_total, b.warp_top, &b.tiles[0]);
+    const int m_total = scan_windows<kExpertsThreads, kTileM>(pr.offsets, pr.P, pr.rows, pr.err, first_m, b.warp_total,
+                                                              b.warp_top, n_tiles, &b.tiles[0]);
     tc_fence_after();
     const uint32_t tmem = b.tmem;
 

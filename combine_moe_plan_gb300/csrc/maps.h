@@ -41,6 +41,20 @@ inline bool tile_map(CUtensorMap* m, CUtensorMapDataType type, const void* base,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map of a dense [rows, width] bf16 tensor whose rows are a product's inner
+// dimension: boxes of box_rows by 128 elements, stored as two blocks of 64
+// elements (128 bytes, 128-byte swizzle) by box_rows.  The coordinates are
+// (0, row, element / 64); a load reads zeros past either end.
+inline bool block_map(CUtensorMap* m, const void* base, size_t rows, int width, int box_rows) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)width / 64}, strides[2] = {(cuuint64_t)width * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2}, steps[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // SMs of the current device (0: none).
 inline int sm_count() {
     int dev = 0, sms = 0;

@@ -95,6 +95,53 @@ __device__ __forceinline__ void mbar_pass(uint32_t bar, uint32_t parity, volatil
     __syncwarp();
 }
 
+// ---- two CTAs of a cluster as a pair: barriers of either CTA.  `addr` is an
+// address of the cluster's shared memory (peer_smem). ----
+__device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {  // `local` as CTA `rank` has it
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Publishes nothing: only TMA's bytes are behind it.  (With release semantics it
+// costs the loading thread some 1000 cycles.)
+__device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t addr, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes)
+                 : "memory");
+}
+// A phase of a barrier of this CTA that threads of the other arrive at.
+struct PairPhase {
+    uint32_t bar, parity;
+    __device__ __forceinline__ bool over() const {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
+    __device__ __forceinline__ bool poll() const {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kPollNs)
+            : "memory");
+        return ok != 0;
+    }
+    __device__ __forceinline__ uint64_t now() const { return now_ns(); }
+};
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    return wait_bounded(PairPhase{smem_u32(bar), parity}, gave_up);
+}
+
 // ---- TMA: one box of a two-dimensional tensor into shared memory; (x, y) is
 // its first element, x in elements of the inner dimension (16-byte aligned) ----
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
@@ -104,6 +151,22 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The same into this CTA's shared memory, counted at a barrier of either CTA of a
+// pair (an address of the cluster's shared memory).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -148,6 +211,16 @@ __device__ __forceinline__ void tmem_alloc_all(uint32_t* slot) {  // whole warp
 }
 __device__ __forceinline__ void tmem_free_all(uint32_t addr) {  // the same whole warp
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(kTmemColumns) : "memory");
+}
+// For a pair: the same warp of both CTAs.
+__device__ __forceinline__ void tmem_alloc_all_pair(uint32_t* slot) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                 "r"(kTmemColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_all_pair(uint32_t addr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(kTmemColumns) : "memory");
 }
 // Order tcgen05 work of this thread against barriers it passes.
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -207,12 +280,23 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool a_mn, 
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(n / 8) << 17) | ((uint32_t)(m / 16) << 24);
 }
-__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// By a pair: one thread of CTA 0 issues, each CTA's shared memory holds half the
+// rows of A and half the columns of B at the same addresses, and each CTA's TMEM
+// gets its half of the rows.
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+// Arrive on `bar` of both CTAs when every tcgen05 operation this thread issued for the pair is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
         : "memory");
 }
 // Arrive on `bar` when every tcgen05 operation this thread issued is done.

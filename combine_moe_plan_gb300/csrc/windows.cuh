@@ -49,11 +49,12 @@ struct TileWalk {
 // First row tile of every expert, in shared memory; returns their number.  A
 // window that leaves the rows, runs backwards or starts before an earlier
 // offset (it could share rows with an earlier window) counts as empty and is
-// reported.  The thread that holds the expert of the CTA's first tile leaves
-// that tile in *first (the loading thread need not look it up).  Whole CTA.
+// reported.  If `first` is given, the thread that holds the expert of the CTA's
+// first tile leaves that tile there (the loading thread need not look it up).
+// Whole CTA.
 template <int THREADS, int TILE_M>
-__device__ __forceinline__ int scan_windows(const int32_t* offsets, int P, int rows, int32_t* err, int n_tiles,
-                                            int* first_m, int* warp_total, int* warp_top, int4* first) {
+__device__ __forceinline__ int scan_windows(const int32_t* offsets, int P, int rows, int32_t* err, int* first_m,
+                                            int* warp_total, int* warp_top, int n_tiles = 1, int4* first = nullptr) {
     constexpr int kWarps = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (P + THREADS - 1) / THREADS;
@@ -100,7 +101,7 @@ __device__ __forceinline__ int scan_windows(const int32_t* offsets, int P, int r
     for (int p = lo; p < hi; ++p) {
         const int m = first_m[p];
         first_m[p] = run;
-        if (m_first >= run && m_first < run + m) {
+        if (first != nullptr && m_first >= run && m_first < run + m) {
             const int a = p == lo ? a0 : offsets[p], b = p == lo ? b0 : offsets[p + 1];
             const int local = (int)blockIdx.x - run * n_tiles, n = local / m, row = a + (local - n * m) * TILE_M;
             *first = make_int4(p, n, row, min(TILE_M, b - row));
