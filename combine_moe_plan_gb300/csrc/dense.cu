@@ -48,7 +48,7 @@ constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
 // 256 x 216 + 128 x 72 = 64,512.
 constexpr int kSumRegs = 216, kOtherRegs = 72;
-constexpr int kStaging = kRowBox * kLine;         // of one warp
+constexpr int kBoxBytes = kRowBox * kLine;
 constexpr int kMostStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -65,7 +65,7 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 // in fp32 (a gradient, a scale, a gate's parts) are therefore summed 256 terms at a
 // time, and those sums added up in registers, rounded to nearest; results in bf16
 // have no use for it.
-__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 4; }
+__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 8; }
 
 struct alignas(16) Barriers {
     uint64_t full[kMostStages], empty[kMostStages];  // stages; full: both CTAs', in the first
@@ -81,10 +81,15 @@ struct alignas(16) Barriers {
     float maxima[2][2][kHalfM];  // up: of gate and up columns, of the two halves of each row
 };
 
-__host__ __device__ constexpr size_t smem_bytes(int stages, int P) {
-    return (size_t)stages * kStageBytes + kSumWarps * kStaging + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
+// Boxes of outputs that a finishing warp holds, and the stages beside them: 224 KB in all.
+__host__ __device__ constexpr int boxes_of(Op op) {
+    return op == Op::kDownBack ? 3 : op == Op::kDown || op == Op::kUpBack ? 1 : 2;
 }
-static_assert(smem_bytes(kMostStages - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
+__host__ __device__ constexpr int stages_of(Op op) { return kMostStages + 1 - boxes_of(op); }
+__host__ __device__ constexpr size_t smem_bytes(Op op, int stages, int P) {
+    return (size_t)stages * kStageBytes + kSumWarps * boxes_of(op) * kBoxBytes + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
+}
+static_assert(smem_bytes(Op::kDown, stages_of(Op::kDown) - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
 
 struct Problem {
     int P, N, K;  // experts, outputs a row, inner size; grad: columns of b and of a
@@ -118,6 +123,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(__float_as_uint(v), __float_as_uint(v)); }
+
 template <bool FIRST>
 __device__ __forceinline__ void take_sums(Sums& s, uint32_t c0, uint32_t c1) {
     uint32_t v[2][16];
@@ -134,63 +146,61 @@ __device__ __forceinline__ void take_sums(Sums& s, uint32_t c0, uint32_t c1) {
     }
 }
 
-// A warp's box on its way out: 32 rows of 128 bytes in shared memory, 16-byte
-// chunk c of row r at c ^ (r mod 8) (the 128-byte swizzle: no bank conflicts when
-// a lane writes its row).
-struct Box {
-    unsigned char* staging;
+// A warp's boxes of outputs on their way out: 32 rows of 128 bytes in shared
+// memory, 16-byte chunk c of row r at c ^ (r mod 8) (the 128-byte swizzle: no bank
+// conflicts when a lane writes its row).
+struct Boxes {
+    unsigned char* base;  // of this warp
     int lane;
 
-    // The last box has been read, by TMA or by this warp.
-    __device__ __forceinline__ void begin() const {
-        if (elect_one()) bulk_wait_read();
+    // All but the last `PENDING` boxes sent have been read, by TMA or by this warp.
+    template <int PENDING>
+    __device__ __forceinline__ void wait() const {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
         __syncwarp();
     }
-    __device__ __forceinline__ void put(int chunk, uint4 v) const {
-        st_shared16(staging + lane * kLine + ((chunk ^ (lane & 7)) << 4), v);
+    __device__ __forceinline__ void put(int box, int chunk, uint4 v) const { put_at(base + box * kBoxBytes, chunk, v); }
+    __device__ __forceinline__ void put_at(unsigned char* box, int chunk, uint4 v) const {
+        st_shared16(box + lane * kLine + ((chunk ^ (lane & 7)) << 4), v);
     }
-    // To (x, row) of the map: by TMA if all 32 rows are wanted, else the first
-    // `rows` of them 16 bytes a lane, to `at` and on by `pitch` bytes a row (a
-    // window ends here, and the next row is another expert's).
-    __device__ __forceinline__ void send(const CUtensorMap* map, int x, int row, int rows, void* at, size_t pitch) const {
+    // This lane's part of the boxes may be read by TMA.
+    __device__ __forceinline__ void ready() const {
         fence_async_shared();
         __syncwarp();
-        if (rows == kRowBox) {
-            if (elect_one()) {
-                tma_store_2d(map, x, row, staging);
-                bulk_commit();
+    }
+    // A box to (x, row) of the map: by TMA if all 32 rows are wanted, else the
+    // first `rows` of them 16 bytes a lane, to `at` and on by `pitch` bytes a row
+    // (a window ends here, and the next row is another expert's).
+    __device__ __forceinline__ void send(int box, const CUtensorMap* map, int x, int row, int rows, void* at, size_t pitch) const {
+        const unsigned char* from = base + box * kBoxBytes;
+        if (rows < kRowBox) {
+            for (int i = lane; i < rows * 8; i += 32) {
+                const int r = i >> 3, c = i & 7;
+                const uint4 v = *reinterpret_cast<const uint4*>(from + r * kLine + ((c ^ (r & 7)) << 4));
+                st16(static_cast<unsigned char*>(at) + r * pitch + c * 16, v);
             }
             __syncwarp();
-            return;
         }
-        for (int i = lane; i < rows * 8; i += 32) {
-            const int r = i >> 3, c = i & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(staging + r * kLine + ((c ^ (r & 7)) << 4));
-            st16(static_cast<unsigned char*>(at) + r * pitch + c * 16, v);
+        if (elect_one()) {
+            if (rows == kRowBox) tma_store_2d(map, x, row, from);
+            bulk_commit();  // also of nothing: wait() counts boxes
         }
         __syncwarp();
     }
 };
 
-// Four E4M3 codes.
-__device__ __forceinline__ float4 unpack_e4m3(uint32_t w) {
-    uint32_t lo, hi;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xffffu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
-    float4 f;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(lo));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.z), "=f"(f.w) : "r"(hi));
-    return f;
-}
-
 // up: a lane has 64 gate and the same 64 up columns of its row; the other 64 are
 // with the warp of the other half, and so the groups' maxima are exchanged.  The
-// codes of a row's 128 gate columns leave from one warp's box, those of its up
-// columns from the other's.
+// codes of a row's 128 gate columns leave from one warp's second box, those of its
+// up columns from the other's.
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
-                                          const Box& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
+                                          const Boxes& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
                                           int quarter, int half, int n, int row, int rows) {
-    box.begin();
+    const bool keep = pr.codes != nullptr;
+    if (keep)
+        box.wait<1>();  // the last tile's first box, not its second
+    else
+        box.wait<0>();
     float top_g = 0.0f, top_u = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -202,15 +212,16 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
             top_g = fmaxf(top_g, fmaxf(fabsf(g.x), fabsf(g.y)));
             top_u = fmaxf(top_u, fmaxf(fabsf(u.x), fabsf(u.y)));
         }
-        box.put(c, make_uint4(h[0], h[1], h[2], h[3]));
+        box.put(0, c, make_uint4(h[0], h[1], h[2], h[3]));
     }
     const int x = n * kGroup + half * 64;
-    box.send(map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
-    if (pr.codes == nullptr) return;
+    box.ready();
+    box.send(0, map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
+    if (!keep) return;
     const int in_tile = quarter * 32 + box.lane;
     maxima[half][0][in_tile] = top_g;
     maxima[half][1][in_tile] = top_u;
-    box.begin();
+    box.wait<1>();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both maxima, both boxes free
     top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
     top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
@@ -220,7 +231,7 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
         // a tiny group is scaled up first, so that 448 / top stays finite
         const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
         const float inv = top > 0.0f ? kE4M3Max / (top * lift) : 0.0f;
-        const Box to = {half == m ? box.staging : other, box.lane};
+        unsigned char* to = (half == m ? box.base : other) + kBoxBytes;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t q[4];
@@ -229,24 +240,25 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
                 const float2 a = s.at(32 * m + 8 * c + 2 * i), b = s.at(32 * m + 8 * c + 2 * i + 1);
                 q[i] = pack_e4m3x2(a.x * lift * inv, a.y * lift * inv) | pack_e4m3x2(b.x * lift * inv, b.y * lift * inv) << 16;
             }
-            to.put(half * 4 + c, make_uint4(q[0], q[1], q[2], q[3]));
+            box.put_at(to, half * 4 + c, make_uint4(q[0], q[1], q[2], q[3]));
         }
     }
     fence_async_shared();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
     const int xc = half * pr.N + n * kGroup;
-    box.send(map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
+    box.send(1, map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
     if (box.lane < rows)
         pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] =
             (half == 0 ? top_g : top_u) / kE4M3Max;
 }
 
-// down, up_back, and grad in bf16.
-__device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Box& box, const Sums& s, int x, int row, int rows,
+// down, up_back, and grad in bf16: two boxes of 64 columns, through BOXES of this warp's.
+template <int BOXES>
+__device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Boxes& box, const Sums& s, int x, int row, int rows,
                                             uint16_t* out, int width) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        box.begin();
+        box.wait<BOXES - 1>();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t q[4];
@@ -255,9 +267,10 @@ __device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Box& b
                 const float2 v = s.at(32 * b + 4 * c + i);
                 q[i] = pack_bf16x2_rn(v.x, v.y);
             }
-            box.put(c, make_uint4(q[0], q[1], q[2], q[3]));
+            box.put(b % BOXES, c, make_uint4(q[0], q[1], q[2], q[3]));
         }
-        box.send(map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
+        box.ready();
+        box.send(b % BOXES, map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
     }
 }
 
@@ -268,87 +281,88 @@ __device__ __forceinline__ uint4 ld_once16(const void* p) {
     return r;
 }
 
+// Two E4M3 codes as floats.
+__device__ __forceinline__ uint64_t unpack_e4m3x2(uint32_t w) {
+    uint32_t h, lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(h));
+    return pack2(lo, hi);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t pair) {
+    const float2 v = unpack2(pair);
+    return pack_bf16x2_rn(v.x, v.y);
+}
+
 // down_back: a lane has one 128-group of its row, whose scales and sum are its own.
+//   s = sigmoid(g), h = g s u, hg = gate h, du = gate d g s, dg = gate d u (s + g s (1 - s))
 __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtensorMap* map_hg, const CUtensorMap* map_dgu,
-                                                 const Box& box, Sums& d, int blk, int row, int rows) {
+                                                 const Boxes& box, const Sums& d, int blk, int row, int rows) {
     const size_t mine = (size_t)row + max(0, min(box.lane, rows - 1));
     const int groups = pr.N / kGroup;
-    const float gate = __ldg(pr.row_gates + mine);
-    const float sg = __ldg(pr.scales + mine * pr.scale_stride + blk);
-    const float su = __ldg(pr.scales + mine * pr.scale_stride + groups + blk);
+    const uint64_t gate = both(__ldg(pr.row_gates + mine));
+    const uint64_t sg = both(__ldg(pr.scales + mine * pr.scale_stride + blk));
+    const uint64_t su = both(__ldg(pr.scales + mine * pr.scale_stride + groups + blk));
+    const uint64_t one = both(1.0f), minus_one = both(-1.0f);
     const uint8_t* codes = pr.codes + mine * 2 * pr.N + blk * kGroup;
     uint4 next_g = ld_once16(codes), next_u = ld_once16(codes + pr.N);
-    float sum = 0.0f;
-    // One half after the other, the second moved to where the first was: unrolled,
-    // this takes more registers than there are.
-#pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
-        uint32_t du[32], hg[32];  // bf16 pairs of 64 columns
-        box.begin();
+    uint64_t sum = 0ull;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 columns
-            const uint4 cg = next_g, cu = next_u;
-            const int next = b * 64 + c * 16 + 16;  // a step ahead, and no further: registers
-            if (next < kGroup) next_g = ld_once16(codes + next), next_u = ld_once16(codes + pr.N + next);
-            const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
-            uint32_t dg[8];
+    for (int b = 0; b < 2; ++b) {
+        box.wait<0>();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // 8 columns
+            if ((c & 1) == 0 && (b > 0 || c > 0)) {
+                next_g = ld_once16(codes + b * 64 + c * 8);
+                next_u = ld_once16(codes + pr.N + b * 64 + c * 8);
+            }
+            const uint32_t wg[2] = {c & 1 ? next_g.z : next_g.x, c & 1 ? next_g.w : next_g.y};
+            const uint32_t wu[2] = {c & 1 ? next_u.z : next_u.x, c & 1 ? next_u.w : next_u.y};
+            uint32_t dg[4], du[4], hg[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float4 fg = unpack_e4m3(wg[q]), fu = unpack_e4m3(wu[q]);
-                const float gs[4] = {fg.x, fg.y, fg.z, fg.w}, us[4] = {fu.x, fu.y, fu.z, fu.w};
-                const float2 d0 = d.at(8 * c + 2 * q), d1 = d.at(8 * c + 2 * q + 1);
-                const float ds[4] = {d0.x, d0.y, d1.x, d1.y};
-                float vg[4], vu[4], vh[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float g = gs[i] * sg, u = us[i] * su, dd = ds[i];
-                    const float s = sigmoid(g), silu = g * s, h = silu * u, dh = gate * dd;
-                    sum += dd * h;
-                    vg[i] = dh * u * (s * (1.0f + g * (1.0f - s)));
-                    vu[i] = dh * silu;
-                    vh[i] = gate * h;
-                }
-                dg[2 * q] = pack_bf16x2_rn(vg[0], vg[1]), dg[2 * q + 1] = pack_bf16x2_rn(vg[2], vg[3]);
-                du[8 * c + 2 * q] = pack_bf16x2_rn(vu[0], vu[1]), du[8 * c + 2 * q + 1] = pack_bf16x2_rn(vu[2], vu[3]);
-                hg[8 * c + 2 * q] = pack_bf16x2_rn(vh[0], vh[1]), hg[8 * c + 2 * q + 1] = pack_bf16x2_rn(vh[2], vh[3]);
+                const uint64_t g = mul2(unpack_e4m3x2(wg[q >> 1] >> (16 * (q & 1))), sg);
+                const uint64_t u = mul2(unpack_e4m3x2(wu[q >> 1] >> (16 * (q & 1))), su);
+                const float2 gs = unpack2(g);
+                const uint64_t sig = pack2(__float_as_uint(sigmoid(gs.x)), __float_as_uint(sigmoid(gs.y)));
+                const uint64_t dd = d.v[32 * b + 4 * c + q], dh = mul2(gate, dd);
+                const uint64_t silu = mul2(g, sig), h = mul2(silu, u);
+                sum = fma2(dd, h, sum);
+                hg[q] = pack_bf16(mul2(gate, h));
+                du[q] = pack_bf16(mul2(dh, silu));
+                dg[q] = pack_bf16(mul2(mul2(dh, u), fma2(silu, fma2(sig, minus_one, one), sig)));
             }
-            box.put(2 * c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
-            box.put(2 * c + 1, make_uint4(dg[4], dg[5], dg[6], dg[7]));
+            box.put(0, c, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+            box.put(1, c, make_uint4(du[0], du[1], du[2], du[3]));
+            box.put(2, c, make_uint4(hg[0], hg[1], hg[2], hg[3]));
         }
         const int x = blk * kGroup + b * 64;
         const size_t wide = (size_t)2 * pr.N;
-        box.send(map_dgu, x, row, rows, pr.dgu + row * wide + x, wide * 2);
-        box.begin();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) box.put(c, make_uint4(du[4 * c], du[4 * c + 1], du[4 * c + 2], du[4 * c + 3]));
-        box.send(map_dgu, pr.N + x, row, rows, pr.dgu + row * wide + pr.N + x, wide * 2);
-        box.begin();
-#pragma unroll
-        for (int c = 0; c < 8; ++c) box.put(c, make_uint4(hg[4 * c], hg[4 * c + 1], hg[4 * c + 2], hg[4 * c + 3]));
-        box.send(map_hg, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) d.v[i] = d.v[32 + i];
+        box.ready();
+        box.send(0, map_dgu, x, row, rows, pr.dgu + row * wide + x, wide * 2);
+        box.send(1, map_dgu, pr.N + x, row, rows, pr.dgu + row * wide + pr.N + x, wide * 2);
+        box.send(2, map_hg, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
     }
-    if (box.lane < rows) pr.parts[mine * groups + blk] = sum;
+    const float2 total = unpack2(sum);
+    if (box.lane < rows) pr.parts[mine * groups + blk] = total.x + total.y;
 }
 
-// grad in fp32: four boxes of 32 columns.
-__device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Box& box, const Sums& s, int x, int row, bool add) {
+// grad in fp32: four boxes of 32 columns, through two.
+__device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Boxes& box, const Sums& s, int x, int row, bool add) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        box.begin();
+        box.wait<1>();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const float2 u = s.at(16 * b + 2 * c), v = s.at(16 * b + 2 * c + 1);
-            box.put(c, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y)));
+            box.put(b & 1, c, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y)));
         }
-        fence_async_shared();
-        __syncwarp();
+        box.ready();
         if (elect_one()) {
             if (add)
-                tma_add_2d(map, x + b * 32, row, box.staging);
+                tma_add_2d(map, x + b * 32, row, box.base + (b & 1) * kBoxBytes);
             else
-                tma_store_2d(map, x + b * 32, row, box.staging);
+                tma_store_2d(map, x + b * 32, row, box.base + (b & 1) * kBoxBytes);
             bulk_commit();
         }
         __syncwarp();
@@ -361,18 +375,18 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
              const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
-    constexpr int kChunk = chunk_of(OP);
+    constexpr int kChunk = chunk_of(OP), kWarpBytes = boxes_of(OP) * kBoxBytes;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int stages = pr.stages;
     // The kernel has no other shared memory, so the base lies on a 1024-byte
     // boundary.  One that does not is refused.
-    if ((smem_u32(smem) & 1023u) != 0 || smem_bytes(stages, pr.P) > dynamic_smem_bytes()) {
+    if ((smem_u32(smem) & 1023u) != 0 || smem_bytes(OP, stages, pr.P) > dynamic_smem_bytes()) {
         grid_dependency_sync();  // no kernel behind this one starts before those in front of it are done
         if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
         return;
     }
     unsigned char* staging = smem + stages * kStageBytes;
-    Barriers& b = *reinterpret_cast<Barriers*>(staging + kSumWarps * kStaging);
+    Barriers& b = *reinterpret_cast<Barriers*>(staging + kSumWarps * kWarpBytes);
     int* first_m = reinterpret_cast<int*>(&b + 1);  // [P + 1]
     volatile int* gave_up = &b.gave_up;
     // Uniform in a warp, and through the shuffle known to be.
@@ -465,7 +479,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // A whole box of rows, or as many small ones as hold any: a few
                 // rows an expert should not cost 16 KB a stage.
                 const int small = !kGrad && t.w <= 64 ? (t.w + kRowBox - 1) / kRowBox : 0;
-                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kStaging : 0);
+                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kBoxBytes : 0);
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
                     unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
@@ -483,7 +497,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
                     } else {
                         for (int i = 0; i < small; ++i)
-                            tma_load_2d_pair(pa + i * kStaging, &map_a_small, inner, t.z + i * kRowBox, bar);
+                            tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, t.z + i * kRowBox, bar);
                     }
                     ++issued;
                     if (++s == stages) {
@@ -570,7 +584,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // Finishing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
         // lane) and one half of the tile's columns.
         const int quarter = warp & 3, half = warp >> 2;
-        const Box box = {staging + warp * kStaging, lane};
+        const Boxes box = {staging + warp * kWarpBytes, lane};
         const uint32_t c0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (OP == Op::kUp ? 64 : kGroup);
         const uint32_t c1 = c0 + (OP == Op::kUp ? kGroup : 64);
         const uint32_t acc_empty = peer_smem(smem_u32(&b.acc_empty[0]), 0);
@@ -603,14 +617,14 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (!ok) break;
             if (!busy) continue;
             if constexpr (OP == Op::kUp)
-                finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kStaging, b.maxima, s, quarter, half, t.y, row,
+                finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kWarpBytes, b.maxima, s, quarter, half, t.y, row,
                           rows);
             else if constexpr (OP == Op::kDownBack)
                 finish_down_back(pr, &map_out, &map_out2, box, s, blk, row, rows);
             else if constexpr (!kGrad)
-                finish_rows(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
+                finish_rows<boxes_of(OP)>(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
             else if (pr.grad == MOE_GRAD_BF16)
-                finish_rows(&map_out, box, s, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
+                finish_rows<boxes_of(OP)>(&map_out, box, s, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
             else if (pr.grad == MOE_GRAD_F32 || t.w > 0)
                 finish_grad(&map_out, box, s, blk * kGroup, row, pr.grad == MOE_GRAD_F32_ADD);
         }
@@ -661,15 +675,15 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
     if (OP == Op::kUp && pr.codes != nullptr) ok = ok && tile_map(&map_out2, kByte, pr.codes, rows, 2 * pr.N, kRowBox);
     if (OP == Op::kDownBack) ok = ok && tile_map(&map_out2, kBf16, pr.dgu, rows, 2 * pr.N, kRowBox);
     if (!ok) return MOE_ERR_CUDA;
-    // Six stages where the prefix of the windows leaves room for them.
-    pr.stages = smem_bytes(kMostStages, pr.P) <= kSmemLimit ? kMostStages : kMostStages - 1;
+    // One stage less where the prefix of the windows leaves no room for it.
+    pr.stages = stages_of(OP) - (smem_bytes(OP, stages_of(OP), pr.P) <= kSmemLimit ? 0 : 1);
     // The same limit for every size, so that callers on several threads do not lower it for each other.
     if (cudaFuncSetAttribute(dense_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return MOE_ERR_CUDA;
     const int sms = sm_count();
     if (sms < 2) return MOE_ERR_CUDA;
     const unsigned pairs = (unsigned)(m_most * n_tiles < sms / 2 ? m_most * n_tiles : sms / 2);
-    return launch_pdl_cluster(0, 2, dense_kernel<OP>, dim3(2 * pairs), dim3(kDenseThreads), smem_bytes(pr.stages, pr.P), s,
+    return launch_pdl_cluster(0, 2, dense_kernel<OP>, dim3(2 * pairs), dim3(kDenseThreads), smem_bytes(OP, pr.stages, pr.P), s,
                               map_a, map_a_small, map_b, map_out, map_out2, pr) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
