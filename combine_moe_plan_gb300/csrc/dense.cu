@@ -81,10 +81,11 @@ struct alignas(16) Barriers {
     float maxima[2][2][kHalfM];  // up: of gate and up columns, of the two halves of each row
 };
 
-// Boxes of outputs that a finishing warp holds, and the stages beside them: 224 KB in all.
-__host__ __device__ constexpr int boxes_of(Op op) {
-    return op == Op::kDownBack ? 3 : op == Op::kDown || op == Op::kUpBack ? 1 : 2;
-}
+// Boxes of outputs that a finishing warp holds, and the stages beside them: 224 KB in
+// all.  A stage more is worth more than a box more where the boxes of a tile can
+// wait for one another (grad of 98,304 rows: 602 us with 6 stages and 1 box, 621
+// with 5 and 2, 661 with 4 and 3); down_back's three leave together.
+__host__ __device__ constexpr int boxes_of(Op op) { return op == Op::kDownBack ? 3 : 1; }
 __host__ __device__ constexpr int stages_of(Op op) { return kMostStages + 1 - boxes_of(op); }
 __host__ __device__ constexpr size_t smem_bytes(Op op, int stages, int P) {
     return (size_t)stages * kStageBytes + kSumWarps * boxes_of(op) * kBoxBytes + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
@@ -153,10 +154,9 @@ struct Boxes {
     unsigned char* base;  // of this warp
     int lane;
 
-    // All but the last `PENDING` boxes sent have been read, by TMA or by this warp.
-    template <int PENDING>
+    // The boxes sent have been read, by TMA or by this warp.
     __device__ __forceinline__ void wait() const {
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+        if (elect_one()) bulk_wait_read();
         __syncwarp();
     }
     __device__ __forceinline__ void put(int box, int chunk, uint4 v) const { put_at(base + box * kBoxBytes, chunk, v); }
@@ -180,10 +180,11 @@ struct Boxes {
                 st16(static_cast<unsigned char*>(at) + r * pitch + c * 16, v);
             }
             __syncwarp();
+            return;
         }
         if (elect_one()) {
-            if (rows == kRowBox) tma_store_2d(map, x, row, from);
-            bulk_commit();  // also of nothing: wait() counts boxes
+            tma_store_2d(map, x, row, from);
+            bulk_commit();
         }
         __syncwarp();
     }
@@ -191,16 +192,12 @@ struct Boxes {
 
 // up: a lane has 64 gate and the same 64 up columns of its row; the other 64 are
 // with the warp of the other half, and so the groups' maxima are exchanged.  The
-// codes of a row's 128 gate columns leave from one warp's second box, those of its
-// up columns from the other's.
+// codes of a row's 128 gate columns leave from one warp's box, those of its up
+// columns from the other's.
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
                                           const Boxes& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
                                           int quarter, int half, int n, int row, int rows) {
-    const bool keep = pr.codes != nullptr;
-    if (keep)
-        box.wait<1>();  // the last tile's first box, not its second
-    else
-        box.wait<0>();
+    box.wait();
     float top_g = 0.0f, top_u = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -217,11 +214,11 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
     const int x = n * kGroup + half * 64;
     box.ready();
     box.send(0, map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
-    if (!keep) return;
+    if (pr.codes == nullptr) return;
     const int in_tile = quarter * 32 + box.lane;
     maxima[half][0][in_tile] = top_g;
     maxima[half][1][in_tile] = top_u;
-    box.wait<1>();
+    box.wait();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both maxima, both boxes free
     top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
     top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
@@ -231,7 +228,7 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
         // a tiny group is scaled up first, so that 448 / top stays finite
         const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
         const float inv = top > 0.0f ? kE4M3Max / (top * lift) : 0.0f;
-        unsigned char* to = (half == m ? box.base : other) + kBoxBytes;
+        unsigned char* to = half == m ? box.base : other;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t q[4];
@@ -246,19 +243,18 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
     fence_async_shared();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
     const int xc = half * pr.N + n * kGroup;
-    box.send(1, map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
+    box.send(0, map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
     if (box.lane < rows)
         pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] =
             (half == 0 ? top_g : top_u) / kE4M3Max;
 }
 
-// down, up_back, and grad in bf16: two boxes of 64 columns, through BOXES of this warp's.
-template <int BOXES>
+// down, up_back, and grad in bf16: two boxes of 64 columns.
 __device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Boxes& box, const Sums& s, int x, int row, int rows,
                                             uint16_t* out, int width) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        box.wait<BOXES - 1>();
+        box.wait();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint32_t q[4];
@@ -267,18 +263,11 @@ __device__ __forceinline__ void finish_rows(const CUtensorMap* map, const Boxes&
                 const float2 v = s.at(32 * b + 4 * c + i);
                 q[i] = pack_bf16x2_rn(v.x, v.y);
             }
-            box.put(b % BOXES, c, make_uint4(q[0], q[1], q[2], q[3]));
+            box.put(0, c, make_uint4(q[0], q[1], q[2], q[3]));
         }
         box.ready();
-        box.send(b % BOXES, map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
+        box.send(0, map, x + b * 64, row, rows, out + (size_t)row * width + x + b * 64, (size_t)width * 2);
     }
-}
-
-// 16 bytes of a line that this lane reads on (L1 keeps the rest of its sector).
-__device__ __forceinline__ uint4 ld_once16(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
 }
 
 // Two E4M3 codes as floats.
@@ -294,30 +283,39 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t pair) {
     return pack_bf16x2_rn(v.x, v.y);
 }
 
+// What finishing a tile of down_back needs of a lane's row besides the codes: loaded
+// while the tile is summed.
+struct RowScalars {
+    float gate, sg, su;
+};
+__device__ __forceinline__ RowScalars row_scalars(const Problem& pr, size_t row, int blk) {
+    const float* scales = pr.scales + row * pr.scale_stride + blk;
+    return {__ldg(pr.row_gates + row), __ldg(scales), __ldg(scales + pr.N / kGroup)};
+}
+
 // down_back: a lane has one 128-group of its row, whose scales and sum are its own.
+// The codes are in L2 by now (the loading thread saw to it when it began the tile);
+// those of 64 columns are loaded at once, so that their latency is paid twice a tile.
 //   s = sigmoid(g), h = g s u, hg = gate h, du = gate d g s, dg = gate d u (s + g s (1 - s))
 __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtensorMap* map_hg, const CUtensorMap* map_dgu,
-                                                 const Boxes& box, const Sums& d, int blk, int row, int rows) {
-    const size_t mine = (size_t)row + max(0, min(box.lane, rows - 1));
-    const int groups = pr.N / kGroup;
-    const uint64_t gate = both(__ldg(pr.row_gates + mine));
-    const uint64_t sg = both(__ldg(pr.scales + mine * pr.scale_stride + blk));
-    const uint64_t su = both(__ldg(pr.scales + mine * pr.scale_stride + groups + blk));
+                                                 const Boxes& box, const Sums& d, const RowScalars& rs, int blk, int row,
+                                                 int rows) {
+    const size_t mine = (size_t)row + min(box.lane, rows - 1);
+    const uint64_t gate = both(rs.gate), sg = both(rs.sg), su = both(rs.su);
     const uint64_t one = both(1.0f), minus_one = both(-1.0f);
-    const uint8_t* codes = pr.codes + mine * 2 * pr.N + blk * kGroup;
-    uint4 next_g = ld_once16(codes), next_u = ld_once16(codes + pr.N);
+    const uint4* codes = reinterpret_cast<const uint4*>(pr.codes + mine * 2 * pr.N + blk * kGroup);
     uint64_t sum = 0ull;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        box.wait<0>();
+        uint4 cg[4], cu[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cg[i] = __ldg(codes + 4 * b + i), cu[i] = __ldg(codes + pr.N / 16 + 4 * b + i);
+        box.wait();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {  // 8 columns
-            if ((c & 1) == 0 && (b > 0 || c > 0)) {
-                next_g = ld_once16(codes + b * 64 + c * 8);
-                next_u = ld_once16(codes + pr.N + b * 64 + c * 8);
-            }
-            const uint32_t wg[2] = {c & 1 ? next_g.z : next_g.x, c & 1 ? next_g.w : next_g.y};
-            const uint32_t wu[2] = {c & 1 ? next_u.z : next_u.x, c & 1 ? next_u.w : next_u.y};
+            const uint4 pg = cg[c >> 1], pu = cu[c >> 1];
+            const uint32_t wg[2] = {c & 1 ? pg.z : pg.x, c & 1 ? pg.w : pg.y};
+            const uint32_t wu[2] = {c & 1 ? pu.z : pu.x, c & 1 ? pu.w : pu.y};
             uint32_t dg[4], du[4], hg[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -344,25 +342,25 @@ __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtens
         box.send(2, map_hg, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
     }
     const float2 total = unpack2(sum);
-    if (box.lane < rows) pr.parts[mine * groups + blk] = total.x + total.y;
+    if (box.lane < rows) pr.parts[mine * (pr.N / kGroup) + blk] = total.x + total.y;
 }
 
-// grad in fp32: four boxes of 32 columns, through two.
+// grad in fp32: four boxes of 32 columns, one after the other.
 __device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Boxes& box, const Sums& s, int x, int row, bool add) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        box.wait<1>();
+        box.wait();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const float2 u = s.at(16 * b + 2 * c), v = s.at(16 * b + 2 * c + 1);
-            box.put(b & 1, c, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y)));
+            box.put(0, c, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y)));
         }
         box.ready();
         if (elect_one()) {
             if (add)
-                tma_add_2d(map, x + b * 32, row, box.base + (b & 1) * kBoxBytes);
+                tma_add_2d(map, x + b * 32, row, box.base);
             else
-                tma_store_2d(map, x + b * 32, row, box.base + (b & 1) * kBoxBytes);
+                tma_store_2d(map, x + b * 32, row, box.base);
             bulk_commit();
         }
         __syncwarp();
@@ -372,7 +370,8 @@ __device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Boxes&
 template <Op OP>
 __global__ void __launch_bounds__(kDenseThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a_small,
-             const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2, const Problem pr) {
+             const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2,
+             const __grid_constant__ CUtensorMap map_codes, const Problem pr) {
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
     constexpr int kChunk = chunk_of(OP), kWarpBytes = boxes_of(OP) * kBoxBytes;
@@ -473,6 +472,9 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 mbar_arrive(&b.known[j % kTileRing]);
                 const bool two = OP == Op::kUp || 2 * t.y + 1 < blocks;
                 const int steps = steps_of(t);
+                if (OP == Op::kDownBack && t.w > 0)
+                    for (int i = 0; i < (two ? 4 : 2); ++i)  // gate and up columns of its blocks
+                        tma_prefetch_2d(&map_codes, (i & 1) * pr.N + (2 * t.y + (i >> 1)) * kGroup, t.z);
                 // This CTA's half of the tile's columns begins at n0.  128 are loaded;
                 // with one block of 128 outputs left the pair takes 64 of each.
                 const int n0 = OP == Op::kUp ? t.y * kGroup + rank * pr.N : t.y * kTileN + rank * (two ? kGroup : 64);
@@ -599,6 +601,8 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const bool busy = rows > 0 && (OP == Op::kUp || blk < blocks);
             const int steps = steps_of(t);
             Sums s;
+            RowScalars rs;
+            if (OP == Op::kDownBack && busy) rs = row_scalars(pr, (size_t)row + min(lane, rows - 1), blk);
             for (int k0 = 0; k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
                 const uint32_t buf = unit & 1;
                 if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_full[buf], (unit >> 1) & 1, gave_up)))) break;
@@ -612,7 +616,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // the accumulator is read: it may be written again
                 tc_fence_before();
                 __syncwarp();
-                if (elect_one()) mbar_arrive_cluster(acc_empty + 8 * buf);
+                if (elect_one()) mbar_signal_cluster(acc_empty + 8 * buf);
             }
             if (!ok) break;
             if (!busy) continue;
@@ -620,11 +624,11 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kWarpBytes, b.maxima, s, quarter, half, t.y, row,
                           rows);
             else if constexpr (OP == Op::kDownBack)
-                finish_down_back(pr, &map_out, &map_out2, box, s, blk, row, rows);
+                finish_down_back(pr, &map_out, &map_out2, box, s, rs, blk, row, rows);
             else if constexpr (!kGrad)
-                finish_rows<boxes_of(OP)>(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
+                finish_rows(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
             else if (pr.grad == MOE_GRAD_BF16)
-                finish_rows<boxes_of(OP)>(&map_out, box, s, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
+                finish_rows(&map_out, box, s, blk * kGroup, row, rows, static_cast<uint16_t*>(pr.dw), pr.N);
             else if (pr.grad == MOE_GRAD_F32 || t.w > 0)
                 finish_grad(&map_out, box, s, blk * kGroup, row, pr.grad == MOE_GRAD_F32_ADD);
         }
@@ -660,7 +664,7 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
                                    : ((long long)pr.rows + kTileM - 1) / kTileM + min(pr.P, pr.rows);
     if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
     const size_t rows = (size_t)pr.rows, n_rows = (size_t)pr.P * pr.N, k_rows = (size_t)pr.P * pr.K;
-    CUtensorMap map_a, map_a_small, map_b, map_out, map_out2;
+    CUtensorMap map_a, map_a_small, map_b, map_out, map_out2, map_codes;
     bool ok = kGrad ? block_map(&map_a, a, rows, pr.K, kStepK)
                     : tile_map(&map_a, kBf16, a, rows, pr.K, kHalfM) && tile_map(&map_a_small, kBf16, a, rows, pr.K, kRowBox);
     if (kGrad) map_a_small = map_a;
@@ -673,7 +677,10 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
         ok = ok && tile_map(&map_out, kBf16, pr.out, rows, pr.N, kRowBox);
     map_out2 = map_out;
     if (OP == Op::kUp && pr.codes != nullptr) ok = ok && tile_map(&map_out2, kByte, pr.codes, rows, 2 * pr.N, kRowBox);
-    if (OP == Op::kDownBack) ok = ok && tile_map(&map_out2, kBf16, pr.dgu, rows, 2 * pr.N, kRowBox);
+    map_codes = map_out2;
+    if (OP == Op::kDownBack)
+        ok = ok && tile_map(&map_out2, kBf16, pr.dgu, rows, 2 * pr.N, kRowBox) &&
+             tile_map(&map_codes, kByte, pr.codes, rows, 2 * pr.N, kHalfM);
     if (!ok) return MOE_ERR_CUDA;
     // One stage less where the prefix of the windows leaves no room for it.
     pr.stages = stages_of(OP) - (smem_bytes(OP, stages_of(OP), pr.P) <= kSmemLimit ? 0 : 1);
@@ -684,7 +691,7 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
     if (sms < 2) return MOE_ERR_CUDA;
     const unsigned pairs = (unsigned)(m_most * n_tiles < sms / 2 ? m_most * n_tiles : sms / 2);
     return launch_pdl_cluster(0, 2, dense_kernel<OP>, dim3(2 * pairs), dim3(kDenseThreads), smem_bytes(OP, pr.stages, pr.P), s,
-                              map_a, map_a_small, map_b, map_out, map_out2, pr) == cudaSuccess
+                              map_a, map_a_small, map_b, map_out, map_out2, map_codes, pr) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
