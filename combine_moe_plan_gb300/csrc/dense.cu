@@ -14,7 +14,10 @@
 // warps read the other accumulator, do what the product ends in, and send it out by
 // TMA, each warp its own 32 rows in boxes of 128 bytes.  A CTA by itself (128 x 256)
 // has to fetch 48 KB for 512 cycles of products, and an SM gets 64 bytes a cycle
-// from L2: 768 cycles.  A pair fetches 32 KB a CTA.
+// from L2: 768 cycles.  A pair fetches 32 KB a CTA.  Few rows an expert are another
+// matter: there the weights' bytes from HBM are the time, and single CTAs, which keep
+// more of them in flight (32 KB a stage instead of 16) and multiply fewer empty rows,
+// are the faster form (PAIR false).
 //   Rows are the M operand of every product with weights.  Weights are read as
 // they lie: where the product runs over a row's inputs (up, down) they are a
 // K-major operand, where it runs over the outputs (down_back, up_back) an MN-major
@@ -35,12 +38,14 @@ namespace moe {
 namespace {
 
 constexpr int kMostExperts = 4096;
-constexpr int kTileM = 256, kTileN = 256, kStepK = 64;
-constexpr int kHalfM = kTileM / 2;                // a CTA's rows (TMEM lanes)
+constexpr int kTileN = 256, kStepK = 64;
+constexpr int kHalfM = 128;                       // a CTA's rows (TMEM lanes)
+__host__ __device__ constexpr int tile_m(bool pair) { return pair ? 2 * kHalfM : kHalfM; }
 constexpr int kRowBox = 32;                       // rows per TMA box of a row operand and of an output
 constexpr int kLine = 128;                        // bytes of a box's row
 constexpr int kABytes = kHalfM * kLine;
-constexpr int kStageBytes = kABytes + kTileN / 2 * kLine;
+// A stage: a CTA's rows, and the tile's columns or its half of them.
+__host__ __device__ constexpr int stage_bytes(bool pair) { return kABytes + (pair ? kTileN / 2 : kTileN) * kLine; }
 constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an operand
 constexpr int kSumWarps = 8;                      // warps that finish tiles
 constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kClearWarp = kSumWarps + 2;
@@ -86,11 +91,14 @@ struct alignas(16) Barriers {
 // wait for one another (grad of 98,304 rows: 602 us with 6 stages and 1 box, 621
 // with 5 and 2, 661 with 4 and 3); down_back's three leave together.
 __host__ __device__ constexpr int boxes_of(Op op) { return op == Op::kDownBack ? 3 : 1; }
-__host__ __device__ constexpr int stages_of(Op op) { return kMostStages + 1 - boxes_of(op); }
-__host__ __device__ constexpr size_t smem_bytes(Op op, int stages, int P) {
-    return (size_t)stages * kStageBytes + kSumWarps * boxes_of(op) * kBoxBytes + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
+__host__ __device__ constexpr int stages_of(Op op, bool pair) {
+    return (224 * 1024 - kSumWarps * boxes_of(op) * kBoxBytes) / stage_bytes(pair);
 }
-static_assert(smem_bytes(Op::kDown, stages_of(Op::kDown) - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
+__host__ __device__ constexpr size_t smem_bytes(Op op, bool pair, int stages, int P) {
+    return (size_t)stages * stage_bytes(pair) + kSumWarps * boxes_of(op) * kBoxBytes + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
+}
+static_assert(stages_of(Op::kDown, true) == kMostStages, "stages that the barriers are for");
+static_assert(smem_bytes(Op::kDown, true, kMostStages - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
 
 struct Problem {
     int P, N, K;  // experts, outputs a row, inner size; grad: columns of b and of a
@@ -197,56 +205,64 @@ struct Boxes {
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
                                           const Boxes& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
                                           int quarter, int half, int n, int row, int rows) {
-    box.wait();
     float top_g = 0.0f, top_u = 0.0f;
+    if (rows > 0) {
+        box.wait();
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint32_t h[4];
+        for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 g = s.at(4 * c + i), u = s.at(32 + 4 * c + i);
-            h[i] = pack_bf16x2_rn(gated(g.x, u.x), gated(g.y, u.y));
-            top_g = fmaxf(top_g, fmaxf(fabsf(g.x), fabsf(g.y)));
-            top_u = fmaxf(top_u, fmaxf(fabsf(u.x), fabsf(u.y)));
+            for (int i = 0; i < 4; ++i) {
+                const float2 g = s.at(4 * c + i), u = s.at(32 + 4 * c + i);
+                h[i] = pack_bf16x2_rn(gated(g.x, u.x), gated(g.y, u.y));
+                top_g = fmaxf(top_g, fmaxf(fabsf(g.x), fabsf(g.y)));
+                top_u = fmaxf(top_u, fmaxf(fabsf(u.x), fabsf(u.y)));
+            }
+            box.put(0, c, make_uint4(h[0], h[1], h[2], h[3]));
         }
-        box.put(0, c, make_uint4(h[0], h[1], h[2], h[3]));
+        const int x = n * kGroup + half * 64;
+        box.ready();
+        box.send(0, map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
     }
-    const int x = n * kGroup + half * 64;
-    box.ready();
-    box.send(0, map_out, x, row, rows, pr.out + (size_t)row * pr.N + x, (size_t)pr.N * 2);
     if (pr.codes == nullptr) return;
+    // Both warps come here for every tile, rows or none.
     const int in_tile = quarter * 32 + box.lane;
     maxima[half][0][in_tile] = top_g;
     maxima[half][1][in_tile] = top_u;
     box.wait();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both maxima, both boxes free
-    top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
-    top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
+    if (rows > 0) {
+        top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
+        top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const float top = m == 0 ? top_g : top_u;
-        // a tiny group is scaled up first, so that 448 / top stays finite
-        const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
-        const float inv = top > 0.0f ? kE4M3Max / (top * lift) : 0.0f;
-        unsigned char* to = half == m ? box.base : other;
+        for (int m = 0; m < 2; ++m) {
+            const float top = m == 0 ? top_g : top_u;
+            // a tiny group is scaled up first, so that 448 / top stays finite
+            const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
+            const float inv = top > 0.0f ? kE4M3Max / (top * lift) : 0.0f;
+            unsigned char* to = half == m ? box.base : other;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t q[4];
+            for (int c = 0; c < 4; ++c) {
+                uint32_t q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 a = s.at(32 * m + 8 * c + 2 * i), b = s.at(32 * m + 8 * c + 2 * i + 1);
-                q[i] = pack_e4m3x2(a.x * lift * inv, a.y * lift * inv) | pack_e4m3x2(b.x * lift * inv, b.y * lift * inv) << 16;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = s.at(32 * m + 8 * c + 2 * i), b = s.at(32 * m + 8 * c + 2 * i + 1);
+                    q[i] = pack_e4m3x2(a.x * lift * inv, a.y * lift * inv) |
+                           pack_e4m3x2(b.x * lift * inv, b.y * lift * inv) << 16;
+                }
+                box.put_at(to, half * 4 + c, make_uint4(q[0], q[1], q[2], q[3]));
             }
-            box.put_at(to, half * 4 + c, make_uint4(q[0], q[1], q[2], q[3]));
         }
+        fence_async_shared();
     }
-    fence_async_shared();
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");
-    const int xc = half * pr.N + n * kGroup;
-    box.send(0, map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
-    if (box.lane < rows)
-        pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] =
-            (half == 0 ? top_g : top_u) / kE4M3Max;
+    if (rows > 0) {
+        const int xc = half * pr.N + n * kGroup;
+        box.send(0, map_codes, xc, row, rows, pr.codes + (size_t)row * 2 * pr.N + xc, (size_t)pr.N * 2);
+        if (box.lane < rows)
+            pr.scales[(size_t)(row + box.lane) * pr.scale_stride + half * (pr.N / kGroup) + n] =
+                (half == 0 ? top_g : top_u) / kE4M3Max;
+    }
 }
 
 // down, up_back, and grad in bf16: two boxes of 64 columns.
@@ -367,7 +383,7 @@ __device__ __forceinline__ void finish_grad(const CUtensorMap* map, const Boxes&
     }
 }
 
-template <Op OP>
+template <Op OP, bool PAIR>
 __global__ void __launch_bounds__(kDenseThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a_small,
              const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_out2,
@@ -375,11 +391,13 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;  // B lies MN-major
     constexpr int kChunk = chunk_of(OP), kWarpBytes = boxes_of(OP) * kBoxBytes;
+    constexpr int kTileM = tile_m(PAIR), kStageBytes = stage_bytes(PAIR);
+    static_assert(PAIR || (OP != Op::kDownBack && !kGrad), "forms that are not needed");
     extern __shared__ __align__(1024) unsigned char smem[];
     const int stages = pr.stages;
     // The kernel has no other shared memory, so the base lies on a 1024-byte
     // boundary.  One that does not is refused.
-    if ((smem_u32(smem) & 1023u) != 0 || smem_bytes(OP, stages, pr.P) > dynamic_smem_bytes()) {
+    if ((smem_u32(smem) & 1023u) != 0 || smem_bytes(OP, PAIR, stages, pr.P) > dynamic_smem_bytes()) {
         grid_dependency_sync();  // no kernel behind this one starts before those in front of it are done
         if (threadIdx.x == 0) set_error(pr.err, MOE_DEVERR_STALL);
         return;
@@ -390,25 +408,29 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     volatile int* gave_up = &b.gave_up;
     // Uniform in a warp, and through the shuffle known to be.
     const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const int pair = PAIR ? blockIdx.x >> 1 : blockIdx.x, pairs = PAIR ? gridDim.x >> 1 : gridDim.x;  // of those that share tiles
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int s = 0; s < stages; ++s) {
-                mbar_init(&b.full[s], 2);
+                mbar_init(&b.full[s], PAIR ? 2 : 1);
                 mbar_init(&b.empty[s], 1);
                 mbar_init(&b.landed[s], 1);
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&b.acc_full[s], 1);
-                mbar_init(&b.acc_empty[s], 2 * kSumWarps);
+                mbar_init(&b.acc_empty[s], (PAIR ? 2 : 1) * kSumWarps);
             }
             for (int i = 0; i < kTileRing; ++i) mbar_init(&b.known[i], 1);
             b.gave_up = 0;
             mbar_init_fence();
         }
         __syncwarp();
-        tmem_alloc_all_pair(&b.tmem);
+        if (PAIR)
+            tmem_alloc_all_pair(&b.tmem);
+        else
+            tmem_alloc_all(&b.tmem);
         tc_fence_before();
     } else if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
@@ -417,7 +439,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         tma_prefetch_map(&map_out);
         tma_prefetch_map(&map_out2);
     }
-    cluster_arrive();
+    if (PAIR) cluster_arrive();
     grid_dependency_sync();
     allow_dependents();
     const int blocks = pr.N / kGroup;  // 128-blocks of outputs
@@ -425,7 +447,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     // its barriers publish the above to this CTA, the cluster's to the other
     const int m_total = scan_windows<kDenseThreads, kGrad ? kStepK : kTileM>(
         pr.offsets, pr.P, pr.rows, pr.err, first_m, b.warp_total, b.warp_top);
-    cluster_wait();
+    if (PAIR) cluster_wait();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
     // at most 2^31: checked by the host
@@ -448,7 +470,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             uint32_t phase = 0, issued = 0;
             bool ok = true;
             TileWalk<kTileM> walk;
-            const uint32_t full = peer_smem(smem_u32(&b.full[0]), 0);
+            const uint32_t full = PAIR ? peer_smem(smem_u32(&b.full[0]), 0) : 0;
             uint32_t j = 0;
             for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
                 // no tile is written any more, so none overwrites one that a
@@ -475,31 +497,50 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 if (OP == Op::kDownBack && t.w > 0)
                     for (int i = 0; i < (two ? 4 : 2); ++i)  // gate and up columns of its blocks
                         tma_prefetch_2d(&map_codes, (i & 1) * pr.N + (2 * t.y + (i >> 1)) * kGroup, t.z);
-                // This CTA's half of the tile's columns begins at n0.  128 are loaded;
-                // with one block of 128 outputs left the pair takes 64 of each.
+                // The columns of this CTA begin at n0.  Of a pair each loads 128; with one
+                // block of 128 outputs left it takes 64 of each.
                 const int n0 = OP == Op::kUp ? t.y * kGroup + rank * pr.N : t.y * kTileN + rank * (two ? kGroup : 64);
                 // A whole box of rows, or as many small ones as hold any: a few
                 // rows an expert should not cost 16 KB a stage.
                 const int small = !kGrad && t.w <= 64 ? (t.w + kRowBox - 1) / kRowBox : 0;
-                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kBoxBytes : 0);
+                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kBoxBytes : 0) -
+                                       (PAIR || two ? 0 : kGroup * kLine);
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
                     unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
-                    uint32_t bar = full + 8 * s;
-                    if (kGrad && t.w > 0 && (k + 1) * kStepK > t.w) bar = peer_smem(smem_u32(&b.landed[s]), rank);
-                    mbar_expect_tx_cluster(bar, bytes);
                     const int inner = k * kStepK;
-                    if constexpr (kBMn)
-                        tma_load_3d_pair(pb, &map_b, 0, (kGrad ? t.z : p * pr.K) + inner, n0 / 64, bar);
-                    else
-                        tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
-                    if constexpr (kGrad) {
-                        tma_load_3d_pair(pa, &map_a, 0, t.z + inner, m0 / 64, bar);
-                    } else if (t.w > 64) {
-                        tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
+                    if constexpr (PAIR) {
+                        uint32_t bar = full + 8 * s;
+                        if (kGrad && t.w > 0 && (k + 1) * kStepK > t.w) bar = peer_smem(smem_u32(&b.landed[s]), rank);
+                        mbar_expect_tx_cluster(bar, bytes);
+                        if constexpr (kBMn)
+                            tma_load_3d_pair(pb, &map_b, 0, (kGrad ? t.z : p * pr.K) + inner, n0 / 64, bar);
+                        else
+                            tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
+                        if constexpr (kGrad) {
+                            tma_load_3d_pair(pa, &map_a, 0, t.z + inner, m0 / 64, bar);
+                        } else if (t.w > 64) {
+                            tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
+                        } else {
+                            for (int i = 0; i < small; ++i)
+                                tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, t.z + i * kRowBox, bar);
+                        }
                     } else {
-                        for (int i = 0; i < small; ++i)
-                            tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, t.z + i * kRowBox, bar);
+                        uint64_t* bar = &b.full[s];
+                        mbar_expect_tx(bar, bytes);
+                        for (int i = 0; i < (two ? 2 : 1); ++i) {  // 128 columns each
+                            if constexpr (kBMn)
+                                tma_load_3d(pb + i * kGroup * kLine, &map_b, 0, p * pr.K + inner, n0 / 64 + 2 * i, bar);
+                            else
+                                tma_load_2d(pb + i * kGroup * kLine, &map_b, inner,
+                                            p * (OP == Op::kUp ? 2 : 1) * pr.N + n0 + i * (OP == Op::kUp ? pr.N : kGroup), bar);
+                        }
+                        if (t.w > 64) {
+                            tma_load_2d(pa, &map_a, inner, t.z, bar);
+                        } else {
+                            for (int i = 0; i < small; ++i)
+                                tma_load_2d(pa + i * kBoxBytes, &map_a_small, inner, t.z + i * kRowBox, bar);
+                        }
                     }
                     ++issued;
                     if (++s == stages) {
@@ -523,6 +564,12 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const uint64_t desc_b = kBMn ? umma_desc_mn(smem + kABytes, kBlockBytes) : umma_desc(smem + kABytes);
             // From one 16 of the inner dimension to the next: 32 bytes along a row, or 16 rows.
             constexpr uint32_t kNextA = kGrad ? 16 * kLine / 16 : 2, kNextB = kBMn ? 16 * kLine / 16 : 2;
+            const auto commit = [](uint64_t* bar) {
+                if (PAIR)
+                    umma_commit_pair(bar);
+                else
+                    umma_commit(bar);
+            };
             int s = 0;
             uint32_t phase = 0, j = 0, unit = 0;  // tiles and chunks of this pair
             for (long long tile = pair; ok && tile < tiles; tile += pairs, ++j) {
@@ -546,14 +593,19 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         const int parts = kGrad ? max(1, min(kStepK / 16, (t.w - k * kStepK + 15) >> 4)) : kStepK / 16;
 #pragma unroll
                         for (int i = 0; i < kStepK / 16; ++i)
-                            if (i < parts) umma_bf16_pair(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
-                        umma_commit_pair(&b.empty[s]);
+                            if (i < parts) {
+                                if (PAIR)
+                                    umma_bf16_pair(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                                else
+                                    umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                            }
+                        commit(&b.empty[s]);
                         if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
                     }
-                    if (ok) umma_commit_pair(&b.acc_full[buf]);
+                    if (ok) commit(&b.acc_full[buf]);
                 }
             }
             if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
@@ -589,12 +641,13 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const Boxes box = {staging + warp * kWarpBytes, lane};
         const uint32_t c0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (OP == Op::kUp ? 64 : kGroup);
         const uint32_t c1 = c0 + (OP == Op::kUp ? kGroup : 64);
-        const uint32_t acc_empty = peer_smem(smem_u32(&b.acc_empty[0]), 0);
+        const uint32_t acc_empty = PAIR ? peer_smem(smem_u32(&b.acc_empty[0]), 0) : smem_u32(&b.acc_empty[0]);
         uint32_t j = 0, unit = 0;
-        bool ok = true;
-        for (long long tile = pair; ok && tile < tiles; tile += pairs, ++j) {
-            if (!(ok = __all_sync(kFull, tile_written(j)))) break;
-            const int4 t = tile_at(j);
+        // These warps run on after a wait has given up (each later wait takes one
+        // poll; the results are void, and reported so): up's pass the same barriers
+        // in every tile.
+        for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
+            const int4 t = __all_sync(kFull, tile_written(j)) ? tile_at(j) : make_int4(kGrad ? -1 : 0, 0, 0, 0);
             const int row = (kGrad ? t.x : t.z) + quarter * 32;
             const int rows = kGrad ? (t.x >= 0 ? kRowBox : 0) : max(0, min(kRowBox, t.w - quarter * 32));
             const int blk = 2 * t.y + half;  // this half's 128 columns (up: of another kind)
@@ -605,7 +658,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (OP == Op::kDownBack && busy) rs = row_scalars(pr, (size_t)row + min(lane, rows - 1), blk);
             for (int k0 = 0; k0 < steps; k0 += min(kChunk, steps - k0), ++unit) {
                 const uint32_t buf = unit & 1;
-                if (!(ok = __all_sync(kFull, mbar_wait(&b.acc_full[buf], (unit >> 1) & 1, gave_up)))) break;
+                mbar_pass(smem_u32(&b.acc_full[buf]), (unit >> 1) & 1, gave_up);
                 tc_fence_after();
                 if (busy) {
                     if (k0 == 0)
@@ -616,14 +669,20 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // the accumulator is read: it may be written again
                 tc_fence_before();
                 __syncwarp();
-                if (elect_one()) mbar_signal_cluster(acc_empty + 8 * buf);
+                if (elect_one()) {
+                    if (PAIR)
+                        mbar_signal_cluster(acc_empty + 8 * buf);
+                    else
+                        mbar_arrive(acc_empty + 8 * buf);
+                }
             }
-            if (!ok) break;
-            if (!busy) continue;
-            if constexpr (OP == Op::kUp)
+            if constexpr (OP == Op::kUp) {
                 finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kWarpBytes, b.maxima, s, quarter, half, t.y, row,
                           rows);
-            else if constexpr (OP == Op::kDownBack)
+                continue;
+            }
+            if (!busy) continue;
+            if constexpr (OP == Op::kDownBack)
                 finish_down_back(pr, &map_out, &map_out2, box, s, rs, blk, row, rows);
             else if constexpr (!kGrad)
                 finish_rows(&map_out, box, s, blk * kGroup, row, rows, pr.out, pr.N);
@@ -640,12 +699,19 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     // Neither CTA leaves while the other may still reach its shared memory or TMEM.
     // (A hardware barrier of threads whose waits have all ended.)
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();
+    if (PAIR) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
-        tmem_free_all_pair(tmem);
+        if (PAIR)
+            tmem_free_all_pair(tmem);
+        else
+            tmem_free_all(tmem);
     }
 }
 
@@ -654,10 +720,11 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 constexpr CUtensorMapDataType kByte = CU_TENSOR_MAP_DATA_TYPE_UINT8, kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                               kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 
-template <Op OP>
-int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t s) {
+template <Op OP, bool PAIR>
+int launch_form(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t s) {
     constexpr bool kGrad = OP == Op::kGrad;
     constexpr bool kBMn = OP == Op::kDownBack || OP == Op::kUpBack || kGrad;
+    constexpr int kTileM = tile_m(PAIR);
     const int blocks = pr.N / kGroup, n_tiles = OP == Op::kUp ? blocks : (blocks + 1) / 2;
     // The most tiles any windows over these rows can have.
     const long long m_most = kGrad ? (long long)pr.P * ((pr.K + kTileM - 1) / kTileM)
@@ -683,17 +750,35 @@ int launch_dense(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t 
              tile_map(&map_codes, kByte, pr.codes, rows, 2 * pr.N, kHalfM);
     if (!ok) return MOE_ERR_CUDA;
     // One stage less where the prefix of the windows leaves no room for it.
-    pr.stages = stages_of(OP) - (smem_bytes(OP, stages_of(OP), pr.P) <= kSmemLimit ? 0 : 1);
+    constexpr int kStages = stages_of(OP, PAIR);
+    pr.stages = kStages - (smem_bytes(OP, PAIR, kStages, pr.P) <= kSmemLimit ? 0 : 1);
+    const auto kernel = dense_kernel<OP, PAIR>;
     // The same limit for every size, so that callers on several threads do not lower it for each other.
-    if (cudaFuncSetAttribute(dense_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const int sms = sm_count();
-    if (sms < 2) return MOE_ERR_CUDA;
-    const unsigned pairs = (unsigned)(m_most * n_tiles < sms / 2 ? m_most * n_tiles : sms / 2);
-    return launch_pdl_cluster(0, 2, dense_kernel<OP>, dim3(2 * pairs), dim3(kDenseThreads), smem_bytes(OP, pr.stages, pr.P), s,
-                              map_a, map_a_small, map_b, map_out, map_out2, map_codes, pr) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    constexpr int kCtas = PAIR ? 2 : 1;
+    const int most = sm_count() / kCtas;
+    if (most < 1) return MOE_ERR_CUDA;
+    const unsigned grid = kCtas * (unsigned)(m_most * n_tiles < most ? m_most * n_tiles : most);
+    const size_t smem = smem_bytes(OP, PAIR, pr.stages, pr.P);
+    const dim3 block(kDenseThreads);
+    const cudaError_t e = PAIR ? launch_pdl_cluster(0, 2, kernel, dim3(grid), block, smem, s, map_a, map_a_small, map_b,
+                                                    map_out, map_out2, map_codes, pr)
+                               : launch_pdl(kernel, dim3(grid), block, smem, s, map_a, map_a_small, map_b, map_out,
+                                            map_out2, map_codes, pr);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Pairs, unless the average window fits a single CTA's rows: then the weights are the
+// time, and single CTAs are faster.  Single CTAs / pairs: up of 1 token over 256
+// experts of 7168 x 2048 80.1 / 86.8 us, down of 96 tokens 933 / 1000, up of 1024
+// tokens over 64 such experts (128 rows each) 606 / 652; 1537 tokens over 44 experts
+// of 1920 x 896 (175 rows each) up 68.5 / 67.5, up_back 71.3 / 67.4.
+template <Op OP>
+int launch_dense(const Problem& pr, const uint16_t* a, const uint16_t* w, cudaStream_t s) {
+    if constexpr (OP == Op::kUp || OP == Op::kDown || OP == Op::kUpBack)
+        if ((long long)pr.rows <= (long long)pr.P * kHalfM) return launch_form<OP, false>(pr, a, w, s);
+    return launch_form<OP, true>(pr, a, w, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
