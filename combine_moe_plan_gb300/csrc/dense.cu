@@ -171,6 +171,12 @@ struct Boxes {
     __device__ __forceinline__ void put_at(unsigned char* box, int chunk, uint4 v) const {
         st_shared16(box + lane * kLine + ((chunk ^ (lane & 7)) << 4), v);
     }
+    __device__ __forceinline__ void put_row(int box, int row, int chunk, uint4 v) const {
+        st_shared16(base + box * kBoxBytes + row * kLine + ((chunk ^ (row & 7)) << 4), v);
+    }
+    __device__ __forceinline__ uint4 get(int box, int chunk) const {
+        return *reinterpret_cast<const uint4*>(base + box * kBoxBytes + lane * kLine + ((chunk ^ (lane & 7)) << 4));
+    }
     // This lane's part of the boxes may be read by TMA.
     __device__ __forceinline__ void ready() const {
         fence_async_shared();
@@ -309,9 +315,27 @@ __device__ __forceinline__ RowScalars row_scalars(const Problem& pr, size_t row,
     return {__ldg(pr.row_gates + row), __ldg(scales), __ldg(scales + pr.N / kGroup)};
 }
 
+// 64 columns of the codes of this warp's 32 rows (gate's, then up's): four lanes a
+// row, so that a load touches 8 lines and not 32.  Lanes past `rows` repeat the last row.
+struct CodeLines {
+    uint4 v[8];
+};
+__device__ __forceinline__ CodeLines load_codes(const Problem& pr, int column, int row, int rows, int lane) {
+    CodeLines c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const size_t r = (size_t)row + min(8 * i + (lane >> 2), rows - 1);
+        const uint8_t* p = pr.codes + r * 2 * pr.N + column + (lane & 3) * 16;
+        c.v[i] = ld_stream16(p);
+        c.v[4 + i] = ld_stream16(p + pr.N);
+    }
+    return c;
+}
+
 // down_back: a lane has one 128-group of its row, whose scales and sum are its own.
-// The codes are in L2 by now (the loading thread saw to it when it began the tile);
-// those of 64 columns are loaded at once, so that their latency is paid twice a tile.
+// The codes are in L2 by now (the loading thread saw to it when it began the tile) and
+// go to their lanes through the third box: a lane's own 128 bytes of it are its row's
+// 64 gate and 64 up codes.
 //   s = sigmoid(g), h = g s u, hg = gate h, du = gate d g s, dg = gate d u (s + g s (1 - s))
 __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtensorMap* map_hg, const CUtensorMap* map_dgu,
                                                  const Boxes& box, const Sums& d, const RowScalars& rs, int blk, int row,
@@ -319,14 +343,19 @@ __device__ __forceinline__ void finish_down_back(const Problem& pr, const CUtens
     const size_t mine = (size_t)row + min(box.lane, rows - 1);
     const uint64_t gate = both(rs.gate), sg = both(rs.sg), su = both(rs.su);
     const uint64_t one = both(1.0f), minus_one = both(-1.0f);
-    const uint4* codes = reinterpret_cast<const uint4*>(pr.codes + mine * 2 * pr.N + blk * kGroup);
     uint64_t sum = 0ull;
+    CodeLines lines = load_codes(pr, blk * kGroup, row, rows, box.lane);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+        box.wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) box.put_row(2, 8 * (i & 3) + (box.lane >> 2), (i >> 2) * 4 + (box.lane & 3), lines.v[i]);
+        __syncwarp();
         uint4 cg[4], cu[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cg[i] = __ldg(codes + 4 * b + i), cu[i] = __ldg(codes + pr.N / 16 + 4 * b + i);
-        box.wait();
+        for (int i = 0; i < 4; ++i) cg[i] = box.get(2, i), cu[i] = box.get(2, 4 + i);
+        __syncwarp();
+        if (b == 0) lines = load_codes(pr, blk * kGroup + 64, row, rows, box.lane);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {  // 8 columns
             const uint4 pg = cg[c >> 1], pu = cu[c >> 1];
