@@ -59,7 +59,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 __device__ __forceinline__ float finite_or_zero(float s) { return s == s ? s : 0.0f; }  // NaN counts as score 0
 
-template <Gates KIND>
+// KEEP: logits a lane holds (softmax scores; at least E / 32).  QUADS: the partial
+// sums are read 16 bytes at a time (their number a multiple of 4).
+template <Gates KIND, int KEEP, bool QUADS>
 __global__ void __launch_bounds__(kGatesThreads)
 gates_backward_kernel(const float* __restrict__ logits, const float* __restrict__ gates,
                       const int32_t* __restrict__ topk_e, const int32_t* __restrict__ slot,
@@ -71,52 +73,72 @@ gates_backward_kernel(const float* __restrict__ logits, const float* __restrict_
     const int t = blockIdx.x * (kGatesThreads / 32) + (threadIdx.x >> 5);
     if (t >= T) return;
     const size_t copy = (size_t)t * k + lane;
-    const int my_slot = lane < k ? slot[copy] : 0, my_e = lane < k ? topk_e[copy] : 0;
+    const bool chosen = lane < k;
+    const int my_slot = chosen ? slot[copy] : 0, my_e = chosen ? topk_e[copy] : 0;
+    const float* row = logits + (size_t)t * E;
+    float l[KEEP];
+    if constexpr (KIND == Gates::kSoftmax) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) l[i] = lane + 32 * i < E ? row[lane + 32 * i] : -INFINITY;
+    }
+    const float gate = KIND == Gates::kPlan && chosen ? gates[copy] : 0.0f;
     if (__any_sync(kFull, my_slot < 0 || my_slot >= T * k || my_e < 0 || my_e >= E)) {
         if (lane == 0) set_error(err, MOE_DEVERR_SLOT);
         return;
     }
+    const float mine = KIND != Gates::kPlan && chosen ? row[my_e] : 0.0f;
 
     // dg of copy `lane`: `lanes` lanes a copy, 32 / lanes copies at a time
     const int in_run = lane & (lanes - 1), run = lane / lanes, runs = 32 / lanes;
     float dg = 0.0f;
     for (int j0 = 0; j0 < k; j0 += runs) {
         const int j = j0 + run;
-        const int s = __shfl_sync(kFull, my_slot, j & 31);
+        const float* p = gate_parts + (size_t)__shfl_sync(kFull, my_slot, j & 31) * parts;
         float sum = 0.0f;
-        if (j < k)
-            for (int b = in_run; b < parts; b += lanes) sum += gate_parts[(size_t)s * parts + b];
+        if (j < k) {
+            if (QUADS) {
+                for (int b = in_run * 4; b < parts; b += lanes * 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(p + b));
+                    sum += (v.x + v.y) + (v.z + v.w);
+                }
+            } else {
+                for (int b = in_run; b < parts; b += lanes) sum += p[b];
+            }
+        }
         for (int off = lanes >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
         // run r holds copy j0 + r: to lane j0 + r
-        const float mine = __shfl_sync(kFull, sum, ((lane - j0) & (runs - 1)) * lanes);
-        if (lane >= j0 && lane < j0 + runs) dg = mine;
+        const float v = __shfl_sync(kFull, sum, ((lane - j0) & (runs - 1)) * lanes);
+        if (lane >= j0 && lane < j0 + runs) dg = v;
     }
-    if (lane < k) dgates[copy] = dg;
-    const bool chosen = lane < k;
-    if (!chosen) dg = 0.0f;
+    if (chosen)
+        dgates[copy] = dg;
+    else
+        dg = 0.0f;
 
     float* out = dlogits + (size_t)t * E;
     if constexpr (KIND == Gates::kPlan) {
-        const float g = chosen ? gates[copy] : 0.0f;
-        const float mean = warp_sum(g * dg);
+        const float mean = warp_sum(gate * dg);
         for (int e = lane; e < E; e += 32) out[e] = 0.0f;
         __syncwarp();
-        if (chosen) out[my_e] = g * (dg - mean);
+        if (chosen) out[my_e] = gate * (dg - mean);
         return;
     }
-    const float* row = logits + (size_t)t * E;
     float top = -INFINITY, total = 0.0f;
     if constexpr (KIND == Gates::kSoftmax) {
-        for (int e = lane; e < E; e += 32) top = fmaxf(top, row[e]);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) top = fmaxf(top, l[i]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-        for (int e = lane; e < E; e += 32) total += finite_or_zero(expf(row[e] - top));
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            l[i] = finite_or_zero(expf(l[i] - top));
+            total += l[i];
+        }
         total = warp_sum(total);
     }
-    const auto score = [&](float l) {
-        return finite_or_zero(KIND == Gates::kSigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) / total);
-    };
-    const float s = chosen ? score(row[my_e]) : 0.0f;
+    const float s = !chosen                    ? 0.0f
+                    : KIND == Gates::kSigmoid  ? finite_or_zero(1.0f / (1.0f + expf(-mine)))
+                                               : finite_or_zero(expf(mine - top) / total);
     float ds = scale * dg;
     if (renorm) {
         const float sum = warp_sum(s);
@@ -129,10 +151,23 @@ gates_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         if (chosen) out[my_e] = ds * s * (1.0f - s);
     } else {
         const float mean = warp_sum(ds * s);
-        for (int e = lane; e < E; e += 32) out[e] = -score(row[e]) * mean;
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (lane + 32 * i < E) out[lane + 32 * i] = -finite_or_zero(l[i] / total) * mean;
         __syncwarp();
         if (chosen) out[my_e] = s * (ds - mean);
     }
+}
+
+using GatesKernel = decltype(&gates_backward_kernel<Gates::kPlan, 1, false>);
+
+template <bool QUADS>
+GatesKernel gates_kernel(const moe_router* router, int E) {
+    if (router == nullptr) return gates_backward_kernel<Gates::kPlan, 1, QUADS>;
+    if (router->score == MOE_SCORE_SIGMOID) return gates_backward_kernel<Gates::kSigmoid, 1, QUADS>;
+    return E <= 64    ? gates_backward_kernel<Gates::kSoftmax, 2, QUADS>
+           : E <= 256 ? gates_backward_kernel<Gates::kSoftmax, 8, QUADS>
+                      : gates_backward_kernel<Gates::kSoftmax, 32, QUADS>;
 }
 
 }  // namespace
@@ -151,11 +186,11 @@ cudaError_t launch_gates_backward(const moe_router* router, const float* logits,
                                   const int32_t* topk_e, const int32_t* slot, const float* gate_parts, int parts,
                                   int T, int E, int k, float* dgates, float* dlogits, int32_t* err, cudaStream_t s,
                                   uint64_t* launches) {
+    const bool quads = parts % 4 == 0;
+    const int loads = quads ? parts / 4 : parts;
     int lanes = 1;
-    while (lanes < 32 && lanes < parts) lanes *= 2;
-    const auto kernel = router == nullptr                      ? gates_backward_kernel<Gates::kPlan>
-                        : router->score == MOE_SCORE_SIGMOID   ? gates_backward_kernel<Gates::kSigmoid>
-                                                               : gates_backward_kernel<Gates::kSoftmax>;
+    while (lanes < 32 && lanes < loads) lanes *= 2;
+    const GatesKernel kernel = quads ? gates_kernel<true>(router, E) : gates_kernel<false>(router, E);
     const bool renorm = router != nullptr && router->renorm != 0;
     const float scale = router != nullptr ? router->scale : 1.0f;
     const int blocks = (T + kGatesThreads / 32 - 1) / (kGatesThreads / 32);
