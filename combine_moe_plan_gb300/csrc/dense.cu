@@ -492,6 +492,15 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     // of zeros (past the end of the rows), so that its gradient is zeros like any other's.
     const auto steps_of = [&](const int4& t) { return kGrad ? max(1, (t.w + kStepK - 1) / kStepK) : pr.K / kStepK; };
 
+    // grad: tile number `tile` as the ring has it (of this CTA's half).
+    const auto grad_tile = [&](long long tile) {
+        const int mn = (int)(tile / n_tiles), p = mn / m_tiles;
+        const int m0 = (mn - p * m_tiles) * kTileM + rank * kHalfM;
+        const int lo = pr.offsets[p], count = first_m[p + 1] > first_m[p] ? pr.offsets[p + 1] - lo : 0;
+        return make_int4(m0 < pr.K ? p * pr.K + m0 : -1, (int)(tile - (long long)mn * n_tiles), count > 0 ? lo : pr.rows,
+                         count);
+    };
+
     if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
         if (elect_one()) {
@@ -506,14 +515,10 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // warp which runs on without waiting is reading
                 if (!(ok = ok && *gave_up == 0)) break;
                 int4 t;
-                int m0 = 0, p;
+                int m0 = 0, p = 0;
                 if constexpr (kGrad) {
-                    const int mn = (int)(tile / n_tiles);
-                    p = mn / m_tiles;
-                    m0 = (mn - p * m_tiles) * kTileM + rank * kHalfM;
-                    const int lo = pr.offsets[p], count = first_m[p + 1] > first_m[p] ? pr.offsets[p + 1] - lo : 0;
-                    t = make_int4(m0 < pr.K ? p * pr.K + m0 : -1, (int)(tile - (long long)mn * n_tiles),
-                                  count > 0 ? lo : pr.rows, count);
+                    t = grad_tile(tile);
+                    m0 = (int)((tile / n_tiles) % m_tiles) * kTileM + rank * kHalfM;
                 } else {
                     const Tile w = walk.at((int)tile, n_tiles, first_m, pr.offsets, pr.P);
                     p = w.p;
@@ -641,10 +646,11 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
     } else if (kGrad && warp == kClearWarp) {
         // The rows past a window in its last stage, cleared up to a multiple of 16.
-        uint32_t j = 0, done = 0, phases = 0;  // steps; a bit a stage
-        for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
-            if (!__all_sync(kFull, tile_written(j))) break;
-            const int4 t = tile_at(j);
+        // (Tiles are worked out here, not read from the ring: nothing holds the ring
+        // up for a warp that has nothing to clear for a while.)
+        uint32_t done = 0, phases = 0;  // steps; a bit a stage
+        for (long long tile = pair; tile < tiles; tile += pairs) {
+            const int4 t = grad_tile(tile);
             const int valid = t.w % kStepK;
             if (valid > 0) {
                 const uint32_t s = (done + t.w / kStepK) % stages;
@@ -672,16 +678,16 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const uint32_t c1 = c0 + (OP == Op::kUp ? kGroup : 64);
         const uint32_t acc_empty = PAIR ? peer_smem(smem_u32(&b.acc_empty[0]), 0) : smem_u32(&b.acc_empty[0]);
         uint32_t j = 0, unit = 0;
-        // These warps run on after a wait has given up (each later wait takes one
-        // poll; the results are void, and reported so): up's pass the same barriers
-        // in every tile.
+        // These warps run on after a wait has given up, so that up's pass the same
+        // barriers in every tile: from the next tile on they have no rows and wait for
+        // no sums (the results are void, and reported so).
         for (long long tile = pair; tile < tiles; tile += pairs, ++j) {
             const int4 t = __all_sync(kFull, tile_written(j)) ? tile_at(j) : make_int4(kGrad ? -1 : 0, 0, 0, 0);
             const int row = (kGrad ? t.x : t.z) + quarter * 32;
             const int rows = kGrad ? (t.x >= 0 ? kRowBox : 0) : max(0, min(kRowBox, t.w - quarter * 32));
             const int blk = 2 * t.y + half;  // this half's 128 columns (up: of another kind)
             const bool busy = rows > 0 && (OP == Op::kUp || blk < blocks);
-            const int steps = steps_of(t);
+            const int steps = __any_sync(kFull, *gave_up != 0) ? 0 : steps_of(t);
             Sums s;
             RowScalars rs;
             if (OP == Op::kDownBack && busy) rs = row_scalars(pr, (size_t)row + min(lane, rows - 1), blk);

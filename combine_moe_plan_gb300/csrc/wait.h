@@ -17,12 +17,12 @@
 
 namespace moe {
 
-constexpr uint32_t kPollNs = 20000;  // a poll may sleep this long (it does for about 4000); it wakes when the phase ends
+constexpr uint32_t kPollNs = 20000;  // a hint: a poll sleeps for about 4000 (33000 with acquire.cluster); it wakes when the phase ends
 constexpr int kStallPolls = 256;     // polls before a wait's clock starts
 constexpr uint64_t kStallNs = MOE_STALL_NS;
 
 // Wait for `phase`: a look, then polls that may sleep.  A wait that is not over
-// after kStallPolls polls (5 ms at most) starts a clock and gives up kStallNs
+// after kStallPolls polls (1 to 8 ms) starts a clock and gives up kStallNs
 // later.  It then sets *gave_up, which every wait reads after each of its polls:
 // those under way return false at their next poll, and each later one that is
 // not over takes one poll.  The clock is not read at first because that takes

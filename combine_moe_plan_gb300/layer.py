@@ -9,7 +9,12 @@ the experts' two products, combine.
     y = moe_layer(x, logits)                             # bf16 [T, H], fp32 [T, E] -> bf16 [T, H]
 
 ``python -m combine_moe_plan_gb300.layer --tokens 96`` times one on random
-weights, call by call and as one CUDA graph.
+weights, call by call and as one CUDA graph; with ``--train`` a TrainingLayer,
+forward and backward:
+
+    net = layer.TrainingLayer(w13, w2, T_max=4096, E=64, k=6)      # bf16 weights
+    y = net.forward(x, logits)                                     # bf16, fp32 -> bf16
+    dx, dlogits = net.backward(dy, dw13, dw2, accumulate=True)     # fp32 gradients, added up
 """
 from __future__ import annotations
 
@@ -86,7 +91,7 @@ class TrainingLayer:
         self.x_rows, self.d_rows = rows(ex.H), rows(ex.H)  # tokens in their windows; their gradients
         self.h, self.dgu = rows(ex.I), rows(2 * ex.I)
         self.parts = rows(ex.I // 128, torch.float32)
-        self.row_gates = torch.empty(n, device=dev)
+        self.row_gates, self.dgates = torch.empty(n, device=dev), torch.empty((T_max, k), device=dev)
         # the pool's error word is zeroed on this stream: before another stream's call may set it
         torch.cuda.current_stream(dev).synchronize()
 
@@ -108,6 +113,8 @@ class TrainingLayer:
             p.plan_routed(logits, self.router, self.bias, self.rep_off, self.rep_ids, buf=buf, stream=stream)
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         v, n = self.views[buf], T * p.k
+        if y is None:
+            y = moe._empty((T, p.H), torch.bfloat16, x.device, stream)
         ex.up(self.x_rows, v["offsets"], self.h, *self.kept[buf], rows=n, stream=stream)
         ex.down(self.h, v["offsets"], v["ex_out"], rows=n, stream=stream)
         y = p.combine(T, y, buf=buf, stream=stream)
@@ -119,16 +126,15 @@ class TrainingLayer:
         if not 0 <= buf < len(self.saved) or self.saved[buf] is None:
             raise ValueError(f"set {buf} has no forward to go back through")
         x, logits = self.saved[buf]
-        T, n, dev = x.shape[0], x.shape[0] * p.k, x.device
-        dx = torch.empty_like(x) if dx is None else dx
-        dlogits = torch.empty_like(logits) if dlogits is None else dlogits
+        T, n = x.shape[0], x.shape[0] * p.k
+        dx = moe._empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
+        dlogits = moe._empty(logits.shape, logits.dtype, x.device, stream) if dlogits is None else dlogits
         moe._dense("dy", dy, torch.bfloat16, (T, p.H))
         moe._dense("dx", dx, torch.bfloat16, (T, p.H))
         moe._dense("dlogits", dlogits, torch.float32, (T, p.E))
         ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
-        dgates = torch.empty((T, p.k), device=dev)
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
         hg = self.h  # the forward's h has been read
         ex.down_backward(self.d_rows, codes, scales, self.row_gates, offsets, self.dgu, hg, self.parts, rows=n,
@@ -139,7 +145,7 @@ class TrainingLayer:
         ex.up_grad(self.dgu, self.x_rows, offsets, dw13, accumulate, rows=n, stream=stream)
         p.gather(T, self.d_rows, dx, buf=buf, stream=stream)
         routed = (None, None) if self.router is None else (self.router, logits)
-        p.gates_backward(T, self.parts, dgates, dlogits, *routed, buf=buf, stream=stream)
+        p.gates_backward(T, self.parts, self.dgates[:T], dlogits, *routed, buf=buf, stream=stream)
         self.saved[buf] = None
         return dx, dlogits
 
@@ -166,15 +172,31 @@ def random_experts(P, H, I, seed=0, device="cuda"):
     return moe.Experts(*pair(2 * I, H), *pair(H, I))
 
 
+def random_dense(P, H, I, seed=0, device="cuda"):
+    """bf16 weights w13 [P, 2 I, H] and w2 [P, H, I], N(0, 1 / inputs)."""
+    g = torch.Generator(device)
+    g.manual_seed(seed)
+
+    def one(n, k):
+        w = torch.empty(P, n, k, dtype=torch.bfloat16, device=device)
+        for p in range(P):
+            w[p] = torch.randn(n, k, generator=g, device=device) * k ** -0.5
+        return w
+
+    return one(2 * I, H), one(H, I)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("tokens", 96), ("hidden", 7168), ("inner", 2048), ("experts", 256), ("topk", 8), ("groups", 8),
                         ("steps", 20)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--train", action="store_true", help="time a TrainingLayer")
     a = ap.parse_args(argv)
     router = moe.Router("sigmoid", n_group=a.groups, topk_group=max(1, a.groups // 2), group_top=2, scale=2.5)
-    layer = ExpertLayer(random_experts(a.experts, a.hidden, a.inner), a.tokens, a.experts, a.topk, router,
-                        bias=torch.zeros(a.experts, device="cuda"))
+    bias = torch.zeros(a.experts, device="cuda")
+    if not a.train:
+        layer = ExpertLayer(random_experts(a.experts, a.hidden, a.inner), a.tokens, a.experts, a.topk, router, bias=bias)
     x = torch.randn(a.tokens, a.hidden, device="cuda").bfloat16()
     logits = torch.randn(a.tokens, a.experts, device="cuda")
     y = torch.empty_like(x)
@@ -190,6 +212,25 @@ def main(argv=None):
         torch.cuda.synchronize()
         return begin.elapsed_time(end) / a.steps * 1e3
 
+    rows = a.tokens * a.topk
+    what = f"{a.tokens} tokens x {a.hidden}, {a.experts} experts of {a.inner}, top-{a.topk} ({rows} rows)"
+    if a.train:
+        w13, w2 = random_dense(a.experts, a.hidden, a.inner)
+        layer = TrainingLayer(w13, w2, a.tokens, a.experts, a.topk, router, bias)
+        dw13, dw2 = torch.empty_like(w13, dtype=torch.float32), torch.empty_like(w2, dtype=torch.float32)
+        dx, dlogits, dy = torch.empty_like(x), torch.empty_like(logits), torch.randn_like(x)
+        forward = timed(lambda: layer.forward(x, logits, y))
+
+        def both():
+            layer.forward(x, logits, y)
+            layer.backward(dy, dw13, dw2, dx, dlogits)
+
+        step = timed(both)
+        if layer.check():
+            raise RuntimeError("device error word set")
+        flops = 18.0 * rows * a.hidden * a.inner  # three products of 6 a row and pair of sizes
+        print(f"{what}: forward {forward:.1f} us, backward {step - forward:.1f} us, {flops / step / 1e6:.0f} TFLOP/s")
+        return
     calls = timed(lambda: layer(x, logits, y))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -197,9 +238,7 @@ def main(argv=None):
     replay = timed(graph.replay)
     if layer.check():
         raise RuntimeError("device error word set")
-    rows = a.tokens * a.topk
-    print(f"{a.tokens} tokens x {a.hidden}, {a.experts} experts of {a.inner}, top-{a.topk} ({rows} rows): "
-          f"{calls:.1f} us a layer call by call, {replay:.1f} us as a graph")
+    print(f"{what}: {calls:.1f} us a layer call by call, {replay:.1f} us as a graph")
 
 
 if __name__ == "__main__":

@@ -324,7 +324,7 @@ class Pool:
         """moe_gather: ``y`` [T, H] = each token's k ``rows`` added up."""
         _tensor("rows", rows, torch.bfloat16, T * self.k, self.H)
         if y is None:
-            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.workspace.device)
+            y = _empty((T, self.H), torch.bfloat16, self.workspace.device, stream)
         _dense("y", y, torch.bfloat16, (T, self.H))
         _on_one_gpu(self.workspace, rows, y)
         _call("moe_gather", self.handle, _ptr(rows), _ptr(y), T, buf, _stream(stream))
@@ -592,6 +592,15 @@ class DenseExperts:
         """Wait for ``stream`` and return the device error word (0 = clean)."""
         (stream or torch.cuda.current_stream()).synchronize()
         return int(self.error_word.item())
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of ``stream``'s (None: the current one's), so that memory which
+    the current stream is done with later than ``stream`` begins is not handed out."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _on_gpu(t):

@@ -183,6 +183,54 @@ def test_captured_and_replayed():
         assert torch.equal(u, v)
 
 
+def test_on_another_stream():
+    """Every call and every new tensor on the given stream, while the current one is busy."""
+    p, q = Problem(200, 256, 128, 8, 2), Problem(200, 256, 128, 8, 2)
+    dw, dv = p.grads(), q.grads()
+    y = p.layer.forward(p.x, p.logits)
+    dx, dl = p.layer.backward(p.dy, *dw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    y2 = q.layer.forward(q.x, q.logits, stream=s)
+    dx2, dl2 = q.layer.backward(q.dy, *dv, stream=s)
+    s.synchronize()
+    for a, b in zip((y, dx, dl, *dw), (y2, dx2, dl2, *dv)):
+        assert torch.equal(a, b)
+    assert p.layer.check() == 0 and q.layer.check() == 0
+
+
+def test_two_layers_on_two_streams_at_once():
+    p = [Problem(300, 384, 256, 8, 3, seed=i) for i in range(2)]
+    want = []
+    for q in p:
+        dw = q.grads()
+        y = q.layer.forward(q.x, q.logits)
+        want.append((y, *q.layer.backward(q.dy, *dw), *dw))
+    streams = [torch.cuda.Stream() for _ in p]
+    got = [None, None]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, q in enumerate(p):
+            dw = want[i][3].clone(), want[i][4].clone()
+            streams[i].wait_stream(torch.cuda.current_stream())
+            y = q.layer.forward(q.x, q.logits, stream=streams[i])
+            got[i] = (y, *q.layer.backward(q.dy, *dw, stream=streams[i]), *dw)
+    torch.cuda.synchronize()
+    for i, q in enumerate(p):
+        assert q.layer.check() == 0
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b)
+
+
+def test_command(capsys):
+    layer.main(["--train", "--tokens", "64", "--hidden", "256", "--inner", "128", "--experts", "8", "--topk", "2",
+                "--groups", "4", "--steps", "2"])
+    assert "backward" in capsys.readouterr().out
+
+
 def test_refusals():
     p = Problem(16, 128, 128, 4, 2)
     dw13, dw2 = p.grads()
