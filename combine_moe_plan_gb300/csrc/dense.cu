@@ -656,11 +656,11 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 const uint32_t s = (done + t.w / kStepK) % stages;
                 if (!__all_sync(kFull, mbar_wait(&b.landed[s], (phases >> s) & 1, gave_up))) break;
                 phases ^= 1u << s;
-                const int chunks = (((valid + 15) & ~15) - valid) * 8, b_blocks = 2 * t.y + 1 < blocks ? 2 : 1;
-                for (int i = lane; i < (2 + b_blocks) * chunks; i += 32) {  // 64-blocks of A, then of B
-                    const int blk = i / chunks, at = i - blk * chunks;
-                    st_shared16(smem + s * kStageBytes + blk * kBlockBytes + valid * kLine + at * 16, make_uint4(0, 0, 0, 0));
-                }
+                unsigned char* at = smem + s * kStageBytes + (lane & 7) * 16;
+                for (int r = valid + (lane >> 3); r < ((valid + 15) & ~15); r += 4)
+#pragma unroll
+                    for (int blk = 0; blk < 4; ++blk)  // 64-blocks of A, then of B
+                        st_shared16(at + blk * kBlockBytes + r * kLine, make_uint4(0, 0, 0, 0));
                 fence_async_shared();
                 __syncwarp();
                 if (elect_one()) mbar_arrive_cluster(peer_smem(smem_u32(&b.full[s]), 0));
