@@ -25,6 +25,25 @@
 // any number.  There a warp clears the last stage's rows past the window in shared
 // memory up to the next multiple of 16 (another expert's rows, or none: a NaN
 // there must not meet a zero), and the rest are left out.
+//
+// What bounds it (one GB300; 98,304 rows over 64 experts of 2048 x 1024 unless named).
+//   up, up_back: the tensor pipe, 92 and 91 % of it active, 544 and 543 cycles a stage
+// of 512; from a cool GPU 485 and 472 us (1.70 and 1.75 PFLOP/s, the rows that fill the
+// last tile of a window not counted), at the power limit, 1.4 to 1.5 GHz, 552 and 533.
+// cuBLAS, 8192 cubed, on the same box: 1.88 and 1.72 PFLOP/s.
+//   grad in fp32: 560 us cool, 603 hot; 65 % of the tensor pipe.  Without its stores
+// (1.07 GB) 475, with operands that stay in L2 as well 441: stores and loads get in
+// each other's way between SM and L2 (43 bytes a cycle in, 7 out).  Stores through
+// the load-store unit instead of TMA 557, 32 bytes a lane straight from registers 674.
+//   down_back: 385 us cool, 393 to 413 hot; 51 % of the tensor pipe.  Finishing a tile
+// takes 17 k of its 31 k cycles and costs 120 of the 385 us: codes in 47, three outputs
+// out 50, arithmetic 20.
+//   Few rows an expert: HBM.  One token over 256 experts of 7168 x 2048, first product
+// 78 to 80 us (69 at the copy peak), 96 tokens, second product 916 to 934 us (6.4 GB:
+// 1.02 of the copy peak).
+//   Measured and left out: L2 prefetches of the operands 8 to 16 stages ahead (603 / 603
+// us of grad, 420 / 410 of down_back); 16 finishing warps in down_back (493 / 413);
+// its boxes 64 bytes wide with a stage more (448 / 413).
 #include <cuda.h>
 
 #include "maps.h"
@@ -67,9 +86,11 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 // Steps that are summed in TMEM before the sums go to registers.  The tensor cores
 // cut their sums off instead of rounding them, which shortens a sum by about
 // 2.4e-8 of it for every 16 terms (98,304 rows over 64 windows: 2.3e-6).  Results
-// in fp32 (a gradient, a scale, a gate's parts) are therefore summed 256 terms at a
-// time, and those sums added up in registers, rounded to nearest; results in bf16
-// have no use for it.
+// in fp32 (a gradient, a scale, a gate's parts) are therefore summed 512 terms at a
+// time, and those sums added up in registers, rounded to nearest: 4.5e-7, as fp32
+// sums are (3.7e-7).  256 terms: 2.3e-7, but the products wait for the finishing
+// warps (up 577 against 552 us); 1024: 1.5e-6 (down_back 383 against 402).  Results in
+// bf16 have no use for it.
 __host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 8; }
 
 struct alignas(16) Barriers {
