@@ -85,12 +85,15 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 
 // Steps that are summed in TMEM before the sums go to registers.  The tensor cores
 // cut their sums off instead of rounding them, which shortens a sum by about
-// 2.4e-8 of it for every 16 terms (98,304 rows over 64 windows: 2.3e-6).  Results
-// in fp32 (a gradient, a scale, a gate's parts) are therefore summed 512 terms at a
-// time, and those sums added up in registers, rounded to nearest: 4.5e-7, as fp32
-// sums are (3.7e-7).  256 terms: 2.3e-7, but the products wait for the finishing
-// warps (up 577 against 552 us); 1024: 1.5e-6 (down_back 383 against 402).  Results in
-// bf16 have no use for it.
+// 2.4e-8 of it for every 16 terms.  Results in fp32 (a gradient, a scale, a gate's
+// parts) are therefore summed 512 terms at a time, and those sums added up in
+// registers, rounded to nearest; results in bf16 have no use for it.  98,304 rows over
+// 64 experts of 2048 x 1024, relative error of up_grad and of down_back's parts (fp32
+// sums: 3.7e-7 and 4e-7), and us of up, down_back and up_grad at the power limit:
+//    256 terms  2.3e-7  2.8e-7  595  441  642
+//    512        4.5e-7  4.9e-7  553  406  611
+//   1024        9.0e-7  1.0e-6  551  388  606
+//   all         2.6e-6  2.1e-6  549  386  605
 __host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 8; }
 
 struct alignas(16) Barriers {
