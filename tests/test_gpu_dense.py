@@ -412,3 +412,86 @@ def test_far_gates():
     assert dgu.isfinite().all() and hg.isfinite().all() and parts.isfinite().all()
     assert (hg[0] == 896).all() and (hg[1] == 0).all() and (hg[3] == 0).all()
     assert (dgu[0, :I] == 2).all() and (dgu[0, I:] == 448).all() and (dgu[1] == 0).all() and (dgu[3] == 0).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_windows(seed):
+    """Sizes, window lengths (skewed, many of them empty), rows in front and behind drawn at random; average
+    windows on both sides of 128 rows, where the products change their form."""
+    r = np.random.default_rng(seed)
+    H, I = (128 * int(r.integers(1, 9)) for _ in range(2))
+    P = int(r.choice([1, 2, 3, 7, 20, 64, 400]))
+    mean = float(r.choice([0.5, 4, 30, 120, 150, 400]))
+    weight = r.gamma(0.7, size=P)
+    sizes = r.poisson(mean * P * weight / weight.sum()) if P * mean < 20000 else r.poisson(mean / 20, size=P)
+    sizes = [int(n) for n in sizes]
+    if sum(sizes) == 0:
+        sizes[-1] = 1
+    first, tail = int(r.integers(0, 40)), int(r.integers(0, 200))
+    if P > 64:
+        H = I = 128
+    check_up(sizes, H, I, first, tail, keep=bool(seed % 3))
+    check_product(sizes, H, I, "down", first, tail)
+    check_product(sizes, H, I, "up", first, tail)
+    check_down_backward(sizes, H, I, first, tail)
+    check_grad(sizes, H, I, "up", "f32", first, tail)
+    check_grad(sizes, H, I, "down", ("add", "bf16")[seed % 2], first, tail)
+
+
+def test_offsets_past_32_bits():
+    """Rows and codes of more than 2^31 elements, the windows at the end of them."""
+    H, I, n = 2048, 1024, 1_100_000
+    g = gen("far")
+    sizes, first = [200, 0, 100], n - 300
+    off = offsets_of(sizes, first)
+    x = torch.empty(n, H, dtype=BF, device="cuda")
+    x[first:] = normal(g, 300, H)
+    ex = moe.DenseExperts(normal(g, 3, 2 * I, H, scale=H ** -0.5), normal(g, 3, H, I, scale=H ** -0.5))
+    h, (codes, scales) = torch.empty(n, I, dtype=BF, device="cuda"), ex.kept(n)
+    ex.up(x, off, h, codes, scales)
+    near = offsets_of(sizes)
+
+    def same(far, close):
+        assert torch.equal(far[first:].view(torch.uint8), close.view(torch.uint8))
+
+    h2, (codes2, scales2) = torch.empty(300, I, dtype=BF, device="cuda"), ex.kept(300)
+    ex.up(x[first:], near, h2, codes2, scales2)
+    same(h, h2)
+    same(codes, codes2)
+    same(scales, scales2)
+    gates = torch.rand(n, generator=g, device="cuda")
+    dgu, hg, parts = (torch.empty(n, w, dtype=t, device="cuda") for w, t in ((2 * I, BF), (I, BF), (I // 128, torch.float32)))
+    dgu2, hg2, parts2 = (t[:300].clone() for t in (dgu, hg, parts))
+    ex.down_backward(x, codes, scales, gates, off, dgu, hg, parts)
+    ex.down_backward(x[first:], codes2, scales2, gates[first:].contiguous(), near, dgu2, hg2, parts2)
+    same(dgu, dgu2)
+    same(hg, hg2)
+    same(parts, parts2)
+    dw, dw2 = (torch.empty(3, 2 * I, H, device="cuda") for _ in range(2))
+    ex.up_grad(dgu, x, off, dw)
+    ex.up_grad(dgu2, x[first:], near, dw2)
+    assert torch.equal(dw, dw2)
+    out, out2 = torch.empty(n, H, dtype=BF, device="cuda"), torch.empty(300, H, dtype=BF, device="cuda")
+    ex.up_backward(dgu, off, out)
+    ex.up_backward(dgu2, near, out2)
+    same(out, out2)
+    ex.down(hg, off, out)
+    ex.down(hg2, near, out2)
+    same(out, out2)
+    assert ex.check() == 0
+
+
+def test_gradients_past_32_bits():
+    """Gradients of more than 2^31 elements: the last experts', and zeros in between."""
+    P, H, I = 1100, 1024, 1024
+    g = gen("far grads")
+    sizes = [3] + [0] * (P - 3) + [70, 5]
+    a, b = normal(g, 78, 2 * I), normal(g, 78, H)
+    dw = torch.full((P, 2 * I, H), 7.0, device="cuda")
+    ex = moe.DenseExperts(sizes=(P, H, I))
+    ex.up_grad(a, b, offsets_of(sizes), dw)
+    assert ex.check() == 0
+    for p, at in windows(sizes, 0):
+        x, y = a[at].double(), b[at].double()
+        within(dw[p], x.T @ y, (at.stop - at.start) * 2.0 ** -23 * (x.abs().T @ y.abs()) + 1e-44)
+    assert not dw[1:P - 2].any()
