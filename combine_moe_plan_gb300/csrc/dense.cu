@@ -107,7 +107,6 @@ struct alignas(16) Barriers {
     uint32_t tmem;
     int gave_up;
     int warp_total[kDenseThreads / 32], warp_top[kDenseThreads / 32];
-    float maxima[2][2][kHalfM];  // up: of gate and up columns, of the two halves of each row
 };
 
 // Boxes of outputs that a finishing warp holds, and the stages beside them: 224 KB in
@@ -122,6 +121,7 @@ __host__ __device__ constexpr size_t smem_bytes(Op op, bool pair, int stages, in
     return (size_t)stages * stage_bytes(pair) + kSumWarps * boxes_of(op) * kBoxBytes + sizeof(Barriers) + (size_t)(P + 1) * sizeof(int);
 }
 static_assert(stages_of(Op::kDown, true) == kMostStages, "stages that the barriers are for");
+static_assert(smem_bytes(Op::kDown, true, kMostStages, 512) <= kSmemLimit, "every stage up to 512 experts and more");
 static_assert(smem_bytes(Op::kDown, true, kMostStages - 1, kMostExperts) <= kSmemLimit, "shared memory of one CTA");
 
 struct Problem {
@@ -229,12 +229,13 @@ struct Boxes {
 };
 
 // up: a lane has 64 gate and the same 64 up columns of its row; the other 64 are
-// with the warp of the other half, and so the groups' maxima are exchanged.  The
+// with the warp of the other half, and so the groups' maxima are exchanged (through
+// the boxes: shared memory of their own would cost a stage from 90 experts on).  The
 // codes of a row's 128 gate columns leave from one warp's box, those of its up
 // columns from the other's.
 __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* map_out, const CUtensorMap* map_codes,
-                                          const Boxes& box, unsigned char* other, float (*maxima)[2][kHalfM], const Sums& s,
-                                          int quarter, int half, int n, int row, int rows) {
+                                          const Boxes& box, unsigned char* other, const Sums& s, int quarter, int half,
+                                          int n, int row, int rows) {
     float top_g = 0.0f, top_u = 0.0f;
     if (rows > 0) {
         box.wait();
@@ -256,14 +257,14 @@ __device__ __forceinline__ void finish_up(const Problem& pr, const CUtensorMap* 
     }
     if (pr.codes == nullptr) return;
     // Both warps come here for every tile, rows or none.
-    const int in_tile = quarter * 32 + box.lane;
-    maxima[half][0][in_tile] = top_g;
-    maxima[half][1][in_tile] = top_u;
     box.wait();
+    reinterpret_cast<float2*>(box.base)[box.lane] = make_float2(top_g, top_u);
     asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both maxima, both boxes free
+    const float2 tops = reinterpret_cast<const float2*>(other)[box.lane];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(64) : "memory");  // both read
     if (rows > 0) {
-        top_g = fmaxf(top_g, maxima[half ^ 1][0][in_tile]);
-        top_u = fmaxf(top_u, maxima[half ^ 1][1][in_tile]);
+        top_g = fmaxf(top_g, tops.x);
+        top_u = fmaxf(top_u, tops.y);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const float top = m == 0 ? top_g : top_u;
@@ -736,7 +737,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             }
             if constexpr (OP == Op::kUp) {
-                finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kWarpBytes, b.maxima, s, quarter, half, t.y, row,
+                finish_up(pr, &map_out, &map_out2, box, staging + (warp ^ 4) * kWarpBytes, s, quarter, half, t.y, row,
                           rows);
                 continue;
             }
