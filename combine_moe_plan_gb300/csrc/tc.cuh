@@ -102,13 +102,14 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {  
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
-// Publishes what this thread wrote to memory before.
+// None of these publishes memory to the other CTA's threads (release.cluster costs the
+// arriving thread 1000 to 2000 cycles, for it waits for the thread's earlier stores):
+// behind the first are this CTA's writes that fence_async_shared has handed to the
+// async proxy, the only reader; behind the second, reads of TMEM that have ended;
+// behind the third, TMA's bytes.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// These publish nothing: behind the one are only reads of TMEM that have ended, behind
-// the other only TMA's bytes.  (Release semantics wait for the thread's earlier
-// stores: some 1000 cycles of the loading thread a stage.)
 __device__ __forceinline__ void mbar_signal_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }

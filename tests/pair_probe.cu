@@ -11,14 +11,14 @@
 
 namespace {
 
-// out[0], out[1]: CTA 0's wait for `rounds` phases of two arrivals of CTA 1 each
-// (one that publishes, one that does not) and what it then read of CTA 1's words;
+// out[0]: whether CTA 0's waits for `rounds` phases, of two arrivals of CTA 1 each,
+// and CTA 1's for one of CTA 0's between them, all ended; out[1]: the rounds;
 // out[2 + rank]: whether the endless wait was left, out[4 + rank]: its time;
 // out[6 + rank]: the longest of eight polls by themselves (how long a poll sleeps is
 // the hardware's choice: the time it is given is a hint).
 __global__ void __cluster_dims__(2, 1, 1) pair_kernel(int rounds, unsigned long long* out) {
     __shared__ uint64_t ready, taken, never;
-    __shared__ int gave_up, word;
+    __shared__ int gave_up;
     const uint32_t rank = moe::cluster_ctarank();
     if (threadIdx.x == 0) {
         moe::mbar_init(&ready, 2);
@@ -26,29 +26,27 @@ __global__ void __cluster_dims__(2, 1, 1) pair_kernel(int rounds, unsigned long 
         moe::mbar_init(&never, 1);
         moe::mbar_init_fence();
         gave_up = 0;
-        word = -1;
     }
     moe::cluster_arrive();
     moe::cluster_wait();
     if (threadIdx.x == 0) {
         const uint32_t there = moe::peer_smem(moe::smem_u32(&ready), 0), back = moe::peer_smem(moe::smem_u32(&taken), 1);
         bool ok = true;
-        unsigned long long sum = 0;
+        unsigned long long done = 0;
         for (int i = 0; ok && i < rounds; ++i) {
             if (rank == 1) {
-                word = i;
                 moe::mbar_signal_cluster(there);
                 moe::mbar_arrive_cluster(there);
                 ok = moe::mbar_wait_pair(&taken, i & 1, &gave_up);
             } else {
                 ok = moe::mbar_wait_pair(&ready, i & 1, &gave_up);
-                sum += moe::ld_cluster_shared_u32(&word, 1);
+                ++done;
                 moe::mbar_arrive_cluster(back);
             }
         }
         if (rank == 0) {
             out[0] = ok;
-            out[1] = sum;
+            out[1] = done;
         }
         uint64_t longest = 0;
         for (int i = 0; i < 8; ++i) {

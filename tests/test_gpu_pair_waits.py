@@ -1,6 +1,5 @@
 """The barriers between the two CTAs of a pair (csrc/tc.cuh) on the GPU: arrivals of
-the other CTA end a wait and publish what was written before, and a wait that nobody
-ends is left."""
+the other CTA end a wait, phase after phase, and a wait that nobody ends is left."""
 import ctypes
 import os
 import shutil
@@ -30,8 +29,8 @@ def test_arrivals_of_the_other_cta_and_a_wait_that_cannot_end(tmp_path):
     got = torch.zeros(8, dtype=torch.int64, device="cuda")
     assert L.pair_run(rounds, got.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
-    ok, total, left0, left1, time0, time1, poll0, poll1 = got.tolist()
-    assert ok == 1 and total == rounds * (rounds - 1) // 2
+    ok, done, left0, left1, time0, time1, poll0, poll1 = got.tolist()
+    assert ok == 1 and done == rounds
     assert left0 == 1 and left1 == 1
     # the polls before the clock (twice the longest of eight each), the limit, and the polls around it
     most = (L.pair_polls() + 3) * 2 * max(poll0, poll1) + LIMIT_NS
