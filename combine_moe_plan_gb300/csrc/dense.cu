@@ -28,22 +28,24 @@
 //
 // What bounds it (one GB300; 98,304 rows over 64 experts of 2048 x 1024 unless named).
 //   up, up_back: the tensor pipe, 92 and 91 % of it active, 544 and 543 cycles a stage
-// of 512; from a cool GPU 485 and 472 us (1.70 and 1.75 PFLOP/s, the rows that fill the
+// of 512; from a cool GPU 480 and 472 us (1.72 and 1.75 PFLOP/s, the rows that fill the
 // last tile of a window not counted), at the power limit, 1.4 to 1.5 GHz, 552 and 533.
 // cuBLAS, 8192 cubed, on the same box: 1.88 and 1.72 PFLOP/s.
-//   grad in fp32: 560 us cool, 603 hot; 65 % of the tensor pipe.  Without its stores
-// (1.07 GB) 475, with operands that stay in L2 as well 441: stores and loads get in
-// each other's way between SM and L2 (43 bytes a cycle in, 7 out).  Stores through
-// the load-store unit instead of TMA 557, 32 bytes a lane straight from registers 674.
-//   down_back: 385 us cool, 393 to 413 hot; 51 % of the tensor pipe.  Finishing a tile
-// takes 17 k of its 31 k cycles and costs 120 of the 385 us: codes in 47, three outputs
-// out 50, arithmetic 20.
+//   grad in fp32: 520 to 530 us cool, 575 to 600 hot.  Its stores (1.07 GB) cost 85 us of
+// it, operands that miss L2 40: stores and loads get in each other's way between SM and
+// L2 (43 bytes a cycle in, 7 out).  Stores through the load-store unit instead of TMA
+// save nothing, 32 bytes a lane straight from registers cost 70 us more.
+//   down_back: 366 us cool, 377 hot; half of the tensor pipe.  Finishing tiles costs 100
+// us: codes in, three outputs out, 16 us of arithmetic.
 //   Few rows an expert: HBM.  One token over 256 experts of 7168 x 2048, first product
-// 78 to 80 us (69 at the copy peak), 96 tokens, second product 916 to 934 us (6.4 GB:
-// 1.02 of the copy peak).
+// 77 us (69 at the copy peak), 96 tokens, second product 897 us (6.4 GB: 1.06 of the copy
+// peak); 4096 tokens over 288, first product 2,623 (1.00).
+//   More stages shorten everything (grad of 24,576 rows in bf16: 185 us with 6, 203 with
+// 5, 250 with 3), so outputs have one box a warp.
 //   Measured and left out: L2 prefetches of the operands 8 to 16 stages ahead (603 / 603
 // us of grad, 420 / 410 of down_back); 16 finishing warps in down_back (493 / 413);
-// its boxes 64 bytes wide with a stage more (448 / 413).
+// its boxes 64 bytes wide with a stage more (448 / 413), or two of them (418 / 381); tiles
+// looked up one ahead (no change).
 #include <cuda.h>
 
 #include "maps.h"
@@ -86,15 +88,19 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 // Steps that are summed in TMEM before the sums go to registers.  The tensor cores
 // cut their sums off instead of rounding them, which shortens a sum by about
 // 2.4e-8 of it for every 16 terms.  Results in fp32 (a gradient, a scale, a gate's
-// parts) are therefore summed 512 terms at a time, and those sums added up in
+// parts) are therefore summed 512 terms at a time (768 in down_back, whose finishing
+// takes longer than the products of two times 512 do), and those sums added up in
 // registers, rounded to nearest; results in bf16 have no use for it.  98,304 rows over
 // 64 experts of 2048 x 1024, relative error of up_grad and of down_back's parts (fp32
 // sums: 3.7e-7 and 4e-7), and us of up, down_back and up_grad at the power limit:
 //    256 terms  2.3e-7  2.8e-7  595  441  642
-//    512        4.5e-7  4.9e-7  553  406  611
-//   1024        9.0e-7  1.0e-6  551  388  606
+//    512        4.5e-7  4.9e-7  553  392 to 406  611
+//    768                6.9e-7       377
+//   1024        9.0e-7  1.0e-6  551  376 to 388  606
 //   all         2.6e-6  2.1e-6  549  386  605
-__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : 8; }
+__host__ __device__ constexpr int chunk_of(Op op) {
+    return op == Op::kDown || op == Op::kUpBack ? 1 << 30 : op == Op::kDownBack ? 12 : 8;
+}
 
 struct alignas(16) Barriers {
     uint64_t full[kMostStages], empty[kMostStages];  // stages; full: both CTAs', in the first
