@@ -134,6 +134,7 @@ class TrainingLayer:
         moe._dense("dlogits", dlogits, torch.float32, (T, p.E))
         ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
+        moe._on_one_gpu(ex.error_word, dw13, dw2)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
         hg = self.h  # the forward's h has been read

@@ -311,8 +311,9 @@ class Pool:
         """moe_scatter: bf16 ``x`` [T, H] into the set's windows of ``rows`` (at
         least T * k rows), unquantized; ``row_gates`` fp32 [at least T * k] gets
         each row's gate.  Both are returned."""
-        T, n = x.shape[0], x.shape[0] * self.k
-        _dense("x", x, torch.bfloat16, (T, self.H))
+        T = x.shape[0]
+        n = T * self.k
+        _shaped("x", x, torch.bfloat16, (T, self.H))
         _tensor("rows", rows, torch.bfloat16, n, self.H)
         if row_gates is not None:
             _vector("row_gates", row_gates, n)
@@ -325,7 +326,7 @@ class Pool:
         _tensor("rows", rows, torch.bfloat16, T * self.k, self.H)
         if y is None:
             y = _empty((T, self.H), torch.bfloat16, self.workspace.device, stream)
-        _dense("y", y, torch.bfloat16, (T, self.H))
+        _shaped("y", y, torch.bfloat16, (T, self.H))
         _on_one_gpu(self.workspace, rows, y)
         _call("moe_gather", self.handle, _ptr(rows), _ptr(y), T, buf, _stream(stream))
         return y
@@ -335,10 +336,10 @@ class Pool:
         the partial sums of ``DenseExperts.down_backward``; ``router`` and
         ``logits`` are those of ``plan_routed``, and left out after ``plan``."""
         parts = _tensor("gate_parts", gate_parts, torch.float32, T * self.k)
-        _dense("dgates", dgates, torch.float32, (T, self.k))
-        _dense("dlogits", dlogits, torch.float32, (T, self.E))
+        _shaped("dgates", dgates, torch.float32, (T, self.k))
+        _shaped("dlogits", dlogits, torch.float32, (T, self.E))
         if logits is not None:
-            _dense("logits", logits, torch.float32, (T, self.E))
+            _shaped("logits", logits, torch.float32, (T, self.E))
         _on_one_gpu(self.workspace, gate_parts, dgates, dlogits, logits)
         _call("moe_gates_backward", self.handle, None if router is None else ctypes.byref(router), _ptr(logits),
               _ptr(gate_parts), parts, T, _ptr(dgates), _ptr(dlogits), buf, _stream(stream))
@@ -490,8 +491,8 @@ class DenseExperts:
             if w is not None:
                 _dense(name, w, torch.bfloat16, shape)
                 device = w.device
-        if w13 is not None and w2 is not None:
-            _on_one_gpu(w13, w2)
+        if w13 is not None and w2 is not None and w13.device != w2.device:
+            raise ValueError(f"w13 is on {w13.device}, w2 on {w2.device}")
         self.w13, self.w2 = w13, w2
         self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
         torch.cuda.current_stream(self.error_word.device).synchronize()  # zero before any stream's kernels may set it
@@ -576,7 +577,7 @@ class DenseExperts:
     def _gradient(self, name, dw, m, n, accumulate):
         if dw.dtype not in (torch.float32, torch.bfloat16) or (accumulate and dw.dtype != torch.float32):
             raise ValueError(f"{name}: want float32, or bfloat16 without accumulate, got {dw.dtype}")
-        _dense(name, dw, dw.dtype, (self.P, m, n))
+        _shaped(name, dw, dw.dtype, (self.P, m, n))
         return GRAD_BF16 if dw.dtype == torch.bfloat16 else GRAD_F32_ADD if accumulate else GRAD_F32
 
     def _codes(self, codes, scales, rows):
@@ -607,18 +608,19 @@ def _on_gpu(t):
     return t.is_cuda
 
 
-def _on_current_gpu(t):
-    return t.is_cuda and t.device.index == _device()
-
-
-def _on_one_gpu(first, *others):
+def _on_one_gpu(*tensors):
     """Every tensor (None: left out) on the current GPU, which the kernels run on."""
-    if not _on_current_gpu(first):
-        raise ValueError(f"want every tensor on the current GPU, got a {first.dtype} {tuple(first.shape)} on {first.device}")
-    device = first.device
-    for t in others:
-        if t is not None and t.device != device:
+    device = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"want every tensor on the current GPU, got a {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _shaped(name, t, dtype, shape):
+    """A contiguous tensor of this type and shape (``_on_one_gpu`` says where)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor {tuple(shape)}, got "
+                         f"{'' if t.is_contiguous() else 'a strided '}{t.dtype} {tuple(t.shape)}")
 
 
 def _vector(name, t, n):

@@ -130,7 +130,7 @@ def test_dense_strides_kinds_and_weights(L):
 def experts(L, monkeypatch):
     """DenseExperts over host tensors that nothing reads."""
     monkeypatch.setattr(moe, "_on_gpu", lambda t: True)
-    monkeypatch.setattr(moe, "_on_current_gpu", lambda t: True)
+    monkeypatch.setattr(moe, "_device", lambda: -1)  # where host tensors say they are
     monkeypatch.setattr(moe, "_stream", lambda stream: None)
     e = moe.DenseExperts.__new__(moe.DenseExperts)
     e.P, e.H, e.I = P, H, I
@@ -188,7 +188,7 @@ def test_binding_odds_and_ends(experts, monkeypatch):
         experts.up_grad(t["dgu"], t["x"], t["offsets"], t["dw13"].to(BF), accumulate=True)
     with pytest.raises(ValueError):
         experts.up(t["x"], t["offsets"], t["h"], rows=N + 1)  # more rows than there are
-    monkeypatch.setattr(moe, "_on_current_gpu", lambda t: False)
+    monkeypatch.setattr(moe, "_device", lambda: 0)
     with pytest.raises(ValueError):
         experts.up(t["x"], t["offsets"], t["h"])
     for bad in (dict(), dict(w13=torch.zeros(2, 256, dtype=BF)), dict(sizes=(2, 200, 128)), dict(sizes=(2, 128, 100)),
@@ -198,14 +198,18 @@ def test_binding_odds_and_ends(experts, monkeypatch):
             moe.DenseExperts(**bad)
 
 
-def test_tensors_of_another_device():
-    here, there = torch.zeros(4), torch.zeros(4, device="meta")
+def test_tensors_of_another_device(monkeypatch):
+    class There:
+        dtype, shape, device = torch.float32, (4,), "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    here = torch.zeros(4)
+    monkeypatch.setattr(moe, "_device", lambda: -1)
+    moe._on_one_gpu(here, None, here)
+    with pytest.raises(ValueError):
+        moe._on_one_gpu(here, There())
+    monkeypatch.setattr(moe, "_device", lambda: 0)
     with pytest.raises(ValueError):
         moe._on_one_gpu(here)  # a host tensor
-    orig, moe._on_current_gpu = moe._on_current_gpu, lambda t: True
-    try:
-        moe._on_one_gpu(here, None, here)
-        with pytest.raises(ValueError):
-            moe._on_one_gpu(here, there)
-    finally:
-        moe._on_current_gpu = orig
