@@ -565,11 +565,14 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 // The columns of this CTA begin at n0.  Of a pair each loads 128; with one
                 // block of 128 outputs left it takes 64 of each.
                 const int n0 = OP == Op::kUp ? t.y * kGroup + rank * pr.N : t.y * kTileN + rank * (two ? kGroup : 64);
-                // A whole box of rows, or as many small ones as hold any: a few
-                // rows an expert should not cost 16 KB a stage.
-                const int small = !kGrad && t.w <= 64 ? (t.w + kRowBox - 1) / kRowBox : 0;
-                const uint32_t bytes = kStageBytes - (!kGrad && t.w <= 64 ? kABytes - small * kBoxBytes : 0) -
-                                       (PAIR || two ? 0 : kGroup * kLine);
+                // A single CTA loads a whole box of rows, or as many small ones as hold any: a
+                // few rows an expert should not cost 16 KB a stage.  A pair clears the boxes
+                // that hold none (by boxes past the end of the rows, which read nothing): the
+                // products of what an earlier tile left there would be thrown away, but not for
+                // free on a GPU that runs at its power limit (up_back of 98,304 rows 538 us / 546).
+                const int small = !kGrad && t.w < kHalfM ? (t.w + kRowBox - 1) / kRowBox : 0;
+                const bool few = !PAIR && t.w <= kHalfM / 2;
+                const uint32_t bytes = kStageBytes - (few ? kABytes - small * kBoxBytes : 0) - (PAIR || two ? 0 : kGroup * kLine);
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = mbar_wait(&b.empty[s], phase ^ 1, gave_up))) break;
                     unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
@@ -584,11 +587,11 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                             tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
                         if constexpr (kGrad) {
                             tma_load_3d_pair(pa, &map_a, 0, t.z + inner, m0 / 64, bar);
-                        } else if (t.w > 64) {
+                        } else if (t.w == kHalfM) {
                             tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
                         } else {
-                            for (int i = 0; i < small; ++i)
-                                tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, t.z + i * kRowBox, bar);
+                            for (int i = 0; i < kHalfM / kRowBox; ++i)
+                                tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, i < small ? t.z + i * kRowBox : pr.rows, bar);
                         }
                     } else {
                         uint64_t* bar = &b.full[s];
@@ -600,7 +603,7 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                                 tma_load_2d(pb + i * kGroup * kLine, &map_b, inner,
                                             p * (OP == Op::kUp ? 2 : 1) * pr.N + n0 + i * (OP == Op::kUp ? pr.N : kGroup), bar);
                         }
-                        if (t.w > 64) {
+                        if (!few) {
                             tma_load_2d(pa, &map_a, inner, t.z, bar);
                         } else {
                             for (int i = 0; i < small; ++i)

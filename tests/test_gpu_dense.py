@@ -495,3 +495,16 @@ def test_gradients_past_32_bits():
         x, y = a[at].double(), b[at].double()
         within(dw[p], x.T @ y, (at.stop - at.start) * 2.0 ** -23 * (x.abs().T @ y.abs()) + 1e-44)
     assert not dw[1:P - 2].any()
+
+
+def test_more_experts_than_every_stage_has_room_for():
+    """The prefix of the windows takes a stage's room: every product, in both forms (a long window among short ones)."""
+    sizes = torch.randint(0, 3, (700,), generator=torch.Generator().manual_seed(1)).tolist()
+    for long in (0, 100_000):
+        sizes[350] = long
+        H = I = 128
+        check_up(sizes, H, I)
+        check_product(sizes, H, I, "down")
+        check_product(sizes, H, I, "up")
+        check_down_backward(sizes, H, I)
+        check_grad(sizes, H, I, "up", "f32")
