@@ -22,9 +22,15 @@
 // they lie: where the product runs over a row's inputs (up, down) they are a
 // K-major operand, where it runs over the outputs (down_back, up_back) an MN-major
 // one, and for grad both operands are: a window's rows are the inner dimension, of
-// any number.  There a warp clears the last stage's rows past the window in shared
-// memory up to the next multiple of 16 (another expert's rows, or none: a NaN
-// there must not meet a zero), and the rest are left out.
+// any number.  There the last stage of a window is loaded with zeros in front of the
+// rows that are left (another expert's rows, or none, lie behind them: a NaN there must
+// not meet a zero), and whole 16 rows of zeros are left out.  The zeros are TMA's, which
+// fills what lies in front of its maps' second dimension (window_map): all of an operand
+// is written by TMA and counted at the issuing CTA's barrier, so that nothing is handed
+// from a thread of one CTA to one of the other.  (A warp that cleared the rows behind a
+// window in shared memory would have to publish them to the other CTA, release.cluster,
+// 1000 to 2200 cycles a tile: 49.5 us of 1537 tokens over 44 experts in bf16; boxes of
+// exactly the rows left, and of zeros behind them, sixteen loads a tile, 50.2.)
 //
 // What bounds it (one GB300; 98,304 rows over 64 experts of 2048 x 1024 unless named).
 //   up, up_back: the tensor pipe, 92 and 91 % of it active, 544 and 543 cycles a stage
@@ -69,7 +75,7 @@ constexpr int kABytes = kHalfM * kLine;
 __host__ __device__ constexpr int stage_bytes(bool pair) { return kABytes + (pair ? kTileN / 2 : kTileN) * kLine; }
 constexpr int kBlockBytes = kStepK * kLine;       // 64 outer elements of an operand
 constexpr int kSumWarps = 8;                      // warps that finish tiles
-constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kClearWarp = kSumWarps + 2;
+constexpr int kTmaWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
 constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // three warpgroups
 // Registers a thread, after setmaxnreg: 64,512 at launch (384 x 168) against
 // 256 x 216 + 128 x 72 = 64,512.
@@ -105,7 +111,6 @@ __host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDownBack ?
 
 struct alignas(16) Barriers {
     uint64_t full[kMostStages], empty[kMostStages];  // stages; full: both CTAs', in the first
-    uint64_t landed[kMostStages];                    // grad: this CTA's half of a stage to be cleared
     uint64_t acc_full[2], acc_empty[2];              // accumulators; empty: both CTAs', in the first
     uint64_t known[kTileRing];                       // tiles[i] is written
     // up .. up_back: expert, n, and of this CTA's half the first row and how many are valid;
@@ -477,7 +482,6 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             for (int s = 0; s < stages; ++s) {
                 mbar_init(&b.full[s], PAIR ? 2 : 1);
                 mbar_init(&b.empty[s], 1);
-                mbar_init(&b.landed[s], 1);
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&b.acc_full[s], 1);
@@ -579,20 +583,23 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     unsigned char *pa = smem + s * kStageBytes, *pb = pa + kABytes;
                     const int inner = k * kStepK;
                     if constexpr (PAIR) {
-                        uint32_t bar = full + 8 * s;
-                        if (kGrad && t.w > 0 && (k + 1) * kStepK > t.w) bar = peer_smem(smem_u32(&b.landed[s]), rank);
+                        const uint32_t bar = full + 8 * s;
                         mbar_expect_tx_cluster(bar, bytes);
-                        if constexpr (kBMn)
-                            tma_load_3d_pair(pb, &map_b, 0, (kGrad ? t.z : p * pr.K) + inner, n0 / 64, bar);
-                        else
-                            tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
                         if constexpr (kGrad) {
-                            tma_load_3d_pair(pa, &map_a, 0, t.z + inner, m0 / 64, bar);
-                        } else if (t.w == kHalfM) {
-                            tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
+                            const int zeros = kStepK - min(kStepK, t.w - inner);  // in front of the window's last rows
+                            tma_load_4d_pair(pb, &map_b, 0, -zeros, t.z + inner, n0 / 64, bar);
+                            tma_load_4d_pair(pa, &map_a, 0, -zeros, t.z + inner, m0 / 64, bar);
                         } else {
-                            for (int i = 0; i < kHalfM / kRowBox; ++i)
-                                tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, i < small ? t.z + i * kRowBox : pr.rows, bar);
+                            if constexpr (kBMn)
+                                tma_load_3d_pair(pb, &map_b, 0, p * pr.K + inner, n0 / 64, bar);
+                            else
+                                tma_load_2d_pair(pb, &map_b, inner, p * (OP == Op::kUp ? 2 : 1) * pr.N + n0, bar);
+                            if (t.w == kHalfM) {
+                                tma_load_2d_pair(pa, &map_a, inner, t.z, bar);
+                            } else {
+                                for (int i = 0; i < kHalfM / kRowBox; ++i)
+                                    tma_load_2d_pair(pa + i * kBoxBytes, &map_a_small, inner, i < small ? t.z + i * kRowBox : pr.rows, bar);
+                            }
                         }
                     } else {
                         uint64_t* bar = &b.full[s];
@@ -652,21 +659,21 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     const int end = k0 + min(kChunk, steps - k0);
                     if (!(ok = mbar_wait_pair(&b.acc_empty[buf], ((unit >> 1) & 1) ^ 1, gave_up))) break;
                     for (int k = k0; k < end; ++k) {
-                        if (!(ok = mbar_wait(&b.full[s], phase, gave_up))) break;
-                        // cleared rows of the other CTA
-                        if (kGrad && (k + 1) * kStepK > t.w) (void)mbar_wait_pair(&b.full[s], phase, gave_up);
+                        // a pair's stage is written by both CTAs' copies
+                        ok = PAIR ? mbar_wait_pair(&b.full[s], phase, gave_up) : mbar_wait(&b.full[s], phase, gave_up);
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t da = desc_a + (uint32_t)s * (kStageBytes / 16);
                         const uint64_t db = desc_b + (uint32_t)s * (kStageBytes / 16);
-                        // the window's last rows: no more than hold any
-                        const int parts = kGrad ? max(1, min(kStepK / 16, (t.w - k * kStepK + 15) >> 4)) : kStepK / 16;
+                        // 16 rows in front of the window's last ones are left out (but one of an empty window's)
+                        const int from = kGrad ? min(kStepK / 16 - 1, max(0, kStepK - (t.w - k * kStepK)) >> 4) : 0;
 #pragma unroll
                         for (int i = 0; i < kStepK / 16; ++i)
-                            if (i < parts) {
+                            if (i >= from) {
                                 if (PAIR)
-                                    umma_bf16_pair(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                                    umma_bf16_pair(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > from);
                                 else
-                                    umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > 0);
+                                    umma_bf16(d, da + i * kNextA, db + i * kNextB, idesc, k > k0 || i > from);
                             }
                         commit(&b.empty[s]);
                         if (++s == stages) {
@@ -679,30 +686,6 @@ dense_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
             if (!ok) set_error(pr.err, MOE_DEVERR_STALL);
         }
-    } else if (kGrad && warp == kClearWarp) {
-        // The rows past a window in its last stage, cleared up to a multiple of 16.
-        // (Tiles are worked out here, not read from the ring: nothing holds the ring
-        // up for a warp that has nothing to clear for a while.)
-        uint32_t done = 0, phases = 0;  // steps; a bit a stage
-        for (long long tile = pair; tile < tiles; tile += pairs) {
-            const int4 t = grad_tile(tile);
-            const int valid = t.w % kStepK;
-            if (valid > 0) {
-                const uint32_t s = (done + t.w / kStepK) % stages;
-                if (!__all_sync(kFull, mbar_wait(&b.landed[s], (phases >> s) & 1, gave_up))) break;
-                phases ^= 1u << s;
-                unsigned char* at = smem + s * kStageBytes + (lane & 7) * 16;
-                for (int r = valid + (lane >> 3); r < ((valid + 15) & ~15); r += 4)
-#pragma unroll
-                    for (int blk = 0; blk < 4; ++blk)  // 64-blocks of A, then of B
-                        st_shared16(at + blk * kBlockBytes + r * kLine, make_uint4(0, 0, 0, 0));
-                fence_async_shared();
-                __syncwarp();
-                if (elect_one()) mbar_arrive_cluster(peer_smem(smem_u32(&b.full[s]), 0));
-            }
-            done += steps_of(t);
-        }
-        if (*gave_up && lane == 0) set_error(pr.err, MOE_DEVERR_STALL);
     } else if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         // Finishing warps: warp w reads TMEM lanes 32 (w mod 4) .. + 31 (a row a
@@ -802,10 +785,10 @@ int launch_form(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t s
     if (m_most * n_tiles > INT32_MAX) return MOE_ERR_SIZE;
     const size_t rows = (size_t)pr.rows, n_rows = (size_t)pr.P * pr.N, k_rows = (size_t)pr.P * pr.K;
     CUtensorMap map_a, map_a_small, map_b, map_out, map_out2, map_codes;
-    bool ok = kGrad ? block_map(&map_a, a, rows, pr.K, kStepK)
+    bool ok = kGrad ? window_map(&map_a, a, rows, pr.K, kStepK)
                     : tile_map(&map_a, kBf16, a, rows, pr.K, kHalfM) && tile_map(&map_a_small, kBf16, a, rows, pr.K, kRowBox);
     if (kGrad) map_a_small = map_a;
-    ok = ok && (kGrad  ? block_map(&map_b, w, rows, pr.N, kStepK)
+    ok = ok && (kGrad  ? window_map(&map_b, w, rows, pr.N, kStepK)
                 : kBMn ? block_map(&map_b, w, k_rows, pr.N, kStepK)
                        : tile_map(&map_b, kBf16, w, (OP == Op::kUp ? 2 : 1) * n_rows, pr.K, kGroup));
     if (kGrad)

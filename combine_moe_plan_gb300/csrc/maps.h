@@ -55,6 +55,21 @@ inline bool block_map(CUtensorMap* m, const void* base, size_t rows, int width, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over a window of rows that ends anywhere: the coordinates are (0, i, row,
+// element / 64) with `window` values of i, and row + i is the row in memory.  A box
+// (window rows) that begins at i = -z has z rows of zeros, then window - z rows from
+// `row` on, and touches no row behind them.
+inline bool window_map(CUtensorMap* m, const void* base, size_t rows, int width, int window) {
+    const EncodeTiledFn encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t pitch = (cuuint64_t)width * 2;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)window, (cuuint64_t)rows, (cuuint64_t)width / 64}, strides[3] = {pitch, pitch, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)window, 1, 2}, steps[4] = {1, 1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // SMs of the current device (0: none).
 inline int sm_count() {
     int dev = 0, sms = 0;

@@ -102,14 +102,17 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {  
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
-// None of these publishes memory to the other CTA's threads (release.cluster costs the
-// arriving thread 1000 to 2000 cycles, for it waits for the thread's earlier stores):
-// behind the first are this CTA's writes that fence_async_shared has handed to the
-// async proxy, the only reader; behind the second, reads of TMEM that have ended;
-// behind the third, TMA's bytes.
+// Publishes what this thread wrote before to a thread of either CTA that waits for the
+// phase (1000 to 2000 cycles of the arriving thread: it waits for its earlier stores).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// These publish nothing, and need not.  Behind the first are reads of TMEM: those are
+// ordered by tcgen05.wait::ld and tcgen05.fence::before_thread_sync in front of the
+// arrival and tcgen05.fence::after_thread_sync behind the wait, with a relaxed arrival
+// between them (the pattern that PTX gives for tcgen05 across threads: memory model,
+// "canonical synchronization patterns").  Behind the second are TMA's writes, which
+// TMA itself counts at the barrier, complete_tx with release at cluster scope.
 __device__ __forceinline__ void mbar_signal_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -183,6 +186,12 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(smem_u32(dst)), "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 
