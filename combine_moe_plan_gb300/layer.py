@@ -107,6 +107,7 @@ class TrainingLayer:
         if y is not None:
             moe._dense("y", y, torch.bfloat16, (T, p.H))
         self.saved[buf] = None
+        self._reads(stream, x, logits)
         if self.router is None:
             p.plan(logits, self.rep_off, self.rep_ids, buf=buf, stream=stream)
         else:
@@ -135,6 +136,7 @@ class TrainingLayer:
         ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
         moe._on_one_gpu(ex.error_word, dw13, dw2)
+        self._reads(stream, dy, x, logits)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
         hg = self.h  # the forward's h has been read
@@ -149,6 +151,14 @@ class TrainingLayer:
         p.gates_backward(T, self.parts, self.dgates[:T], dlogits, *routed, buf=buf, stream=stream)
         self.saved[buf] = None
         return dx, dlogits
+
+    @staticmethod
+    def _reads(stream, *tensors):
+        """``stream`` (None: the current one) reads these: their memory is not handed out again before it has,
+        even if the layer's is the last reference and is let go of while that work is still queued."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        for t in tensors:
+            t.record_stream(s)
 
     def check(self) -> int:
         """Wait, and return the device error bits of the pool and the experts (0 = clean)."""
