@@ -66,8 +66,8 @@ class TrainingLayer:
     routing, bf16 rows, the experts' products, combine; and back.
 
     ``forward`` keeps, per buffer set, x (by reference: leave it alone until the
-    set's ``backward``), the plan, and the experts' gate and up values in 8 bits;
-    rows and experts' outputs are not kept.  ``backward`` takes the gradient of y
+    set's ``backward``), the plan, with a router a copy of the logits, and the
+    experts' gate and up values in 8 bits; rows and experts' outputs are not kept.  ``backward`` takes the gradient of y
     and returns those of x and the logits; the weights' gradients go to ``dw13``
     and ``dw2`` (fp32, added up with ``accumulate``; or bf16).  A replica's weights
     have a gradient of their own.  Several sets may be forward before the first
@@ -84,6 +84,8 @@ class TrainingLayer:
         n, dev = T_max * k, ex.error_word.device
         self.kept = [ex.kept(n) for _ in range(n_sets)]
         self.saved = [None] * n_sets
+        # the logits as the plan saw them: the caller's may be those of the next batch by the time of a backward
+        self.logits = [torch.empty((T_max, E), device=dev) if router is not None else None for _ in range(n_sets)]
 
         def rows(width, dtype=torch.bfloat16):
             return torch.empty((n, width), dtype=dtype, device=dev)
@@ -112,6 +114,8 @@ class TrainingLayer:
             p.plan(logits, self.rep_off, self.rep_ids, buf=buf, stream=stream)
         else:
             p.plan_routed(logits, self.router, self.bias, self.rep_off, self.rep_ids, buf=buf, stream=stream)
+            with torch.cuda.stream(stream):  # (None: the current one)
+                self.logits[buf][:T].copy_(logits)
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         v, n = self.views[buf], T * p.k
         if y is None:
@@ -119,24 +123,24 @@ class TrainingLayer:
         ex.up(self.x_rows, v["offsets"], self.h, *self.kept[buf], rows=n, stream=stream)
         ex.down(self.h, v["offsets"], v["ex_out"], rows=n, stream=stream)
         y = p.combine(T, y, buf=buf, stream=stream)
-        self.saved[buf] = (x, logits)
+        self.saved[buf] = x
         return y
 
     def backward(self, dy, dw13, dw2, dx=None, dlogits=None, accumulate=False, buf=0, stream=None):
         p, ex = self.pool, self.experts
         if not 0 <= buf < len(self.saved) or self.saved[buf] is None:
             raise ValueError(f"set {buf} has no forward to go back through")
-        x, logits = self.saved[buf]
+        x = self.saved[buf]
         T, n = x.shape[0], x.shape[0] * p.k
         dx = moe._empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
-        dlogits = moe._empty(logits.shape, logits.dtype, x.device, stream) if dlogits is None else dlogits
+        dlogits = moe._empty((T, p.E), torch.float32, x.device, stream) if dlogits is None else dlogits
         moe._dense("dy", dy, torch.bfloat16, (T, p.H))
         moe._dense("dx", dx, torch.bfloat16, (T, p.H))
         moe._dense("dlogits", dlogits, torch.float32, (T, p.E))
         ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
         moe._on_one_gpu(ex.error_word, dw13, dw2)
-        self._reads(stream, dy, x, logits)
+        self._reads(stream, dy, x)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
         hg = self.h  # the forward's h has been read
@@ -147,7 +151,7 @@ class TrainingLayer:
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         ex.up_grad(self.dgu, self.x_rows, offsets, dw13, accumulate, rows=n, stream=stream)
         p.gather(T, self.d_rows, dx, buf=buf, stream=stream)
-        routed = (None, None) if self.router is None else (self.router, logits)
+        routed = (None, None) if self.router is None else (self.router, self.logits[buf][:T])
         p.gates_backward(T, self.parts, self.dgates[:T], dlogits, *routed, buf=buf, stream=stream)
         self.saved[buf] = None
         return dx, dlogits

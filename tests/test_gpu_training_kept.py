@@ -76,3 +76,31 @@ def test_tensors_let_go_of_while_another_stream_has_yet_to_read_them(fields, ins
     for got, want in ((y, y0), (dx, dx0), (dl, dl0), (dw13, want13), (dw2, want2)):
         assert torch.equal(got, want)
     del fresh
+
+
+@pytest.mark.parametrize("fields", [None, dict(score="softmax"), dict(score="sigmoid", scale=2.5),
+                                    dict(score="softmax", renorm=False)], ids=str)
+def test_logits_written_over_before_the_backward(fields):
+    """Two batches whose logits come in the same buffer, both forward before either goes back."""
+    T = 96
+    router = moe.Router(**fields) if fields else None
+    lay = net(T, router, n_sets=2)
+    xs, dys = [normal(T, H).to(BF), normal(T, H, scale=2).to(BF)], [normal(T, H, scale=0.5).to(BF), normal(T, H, scale=0.1).to(BF)]
+    ls = [normal(T, E), normal(T, E, scale=3)]
+    want = []
+    for x, l, dy in zip(xs, ls, dys):
+        y = lay.forward(x, l)
+        dw = gradients()
+        want.append((y, *lay.backward(dy, *dw), *dw))
+    buffer = torch.empty(T, E, device="cuda")
+    ys = []
+    for b in range(2):
+        buffer.copy_(ls[b])
+        ys.append(lay.forward(xs[b], buffer, buf=b))
+    buffer.fill_(float("nan"))
+    for b in range(2):
+        dw = gradients()
+        got = (ys[b], *lay.backward(dys[b], *dw, buf=b), *dw)
+        for u, v in zip(got, want[b]):
+            assert torch.equal(u, v)
+    assert lay.check() == 0
