@@ -134,12 +134,14 @@ class TrainingLayer:
         T, n = x.shape[0], x.shape[0] * p.k
         dx = moe._empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
         dlogits = moe._empty((T, p.E), torch.float32, x.device, stream) if dlogits is None else dlogits
+        # all of it before the first launch: a refusal later on would leave gradients added up once already
         moe._dense("dy", dy, torch.bfloat16, (T, p.H))
         moe._dense("dx", dx, torch.bfloat16, (T, p.H))
         moe._dense("dlogits", dlogits, torch.float32, (T, p.E))
         ex._gradient("dw13", dw13, 2 * ex.I, ex.H, accumulate)
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
-        moe._on_one_gpu(ex.error_word, dw13, dw2)
+        moe._on_one_gpu(ex.error_word, dy, dx, dlogits, dw13, dw2)
+        moe._aligned(dy=dy, dx=dx, dlogits=dlogits, dw13=dw13, dw2=dw2)
         self._reads(stream, dy, x)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)

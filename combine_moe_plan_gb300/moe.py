@@ -616,6 +616,13 @@ def _on_one_gpu(*tensors):
             raise ValueError(f"want every tensor on the current GPU, got a {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _aligned(**tensors):
+    """Every tensor begins on a 16-byte boundary, as the kernels want it."""
+    for name, t in tensors.items():
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name}: want a tensor on a 16-byte boundary, got one at {t.data_ptr():#x}")
+
+
 def _shaped(name, t, dtype, shape):
     """A contiguous tensor of this type and shape (``_on_one_gpu`` says where)."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():

@@ -104,3 +104,23 @@ def test_logits_written_over_before_the_backward(fields):
         for u, v in zip(got, want[b]):
             assert torch.equal(u, v)
     assert lay.check() == 0
+
+
+def test_a_refused_backward_adds_nothing_up():
+    """An output that the last call would refuse: the gradients are as they were, and the call repeated with a
+    good one adds them up once."""
+    T = 40
+    lay = net(T)
+    x, l, dy = normal(T, H).to(BF), normal(T, E), normal(T, H, scale=0.5).to(BF)
+    lay.forward(x, l)
+    dw13, dw2 = (torch.full_like(t, 2.0) for t in gradients())
+    odd = torch.empty(T * E + 4, device="cuda")[1:1 + T * E].view(T, E)
+    with pytest.raises(ValueError):
+        lay.backward(dy, dw13, dw2, dlogits=odd, accumulate=True)
+    assert (dw13 == 2).all() and (dw2 == 2).all()
+    lay.backward(dy, dw13, dw2, accumulate=True)
+    want13, want2 = (torch.full_like(t, 2.0) for t in gradients())
+    lay.forward(x, l)
+    lay.backward(dy, want13, want2, accumulate=True)
+    assert torch.equal(dw13, want13) and torch.equal(dw2, want2)
+    assert lay.check() == 0

@@ -1,0 +1,88 @@
+"""layer.TrainingLayer refuses what it cannot take before it enqueues anything.
+
+There is no GPU here: host tensors stand for device tensors, and a pool and experts
+that note their calls for the real ones."""
+import pytest
+import torch
+
+from combine_moe_plan_gb300 import layer, moe
+
+T, H, I, E, P, K = 8, 256, 128, 6, 6, 2
+BF = torch.bfloat16
+
+
+class Recorder:
+    """Notes its calls."""
+
+    def __init__(self, calls, **fields):
+        self.calls = calls
+        self.__dict__.update(fields)
+
+    def __getattr__(self, name):
+        if name.startswith("_"):
+            raise AttributeError(name)
+        return lambda *a, **k: self.calls.append(name)
+
+
+@pytest.fixture
+def net(monkeypatch):
+    """A TrainingLayer after a forward of T tokens, whose calls are noted."""
+    monkeypatch.setattr(moe, "_on_gpu", lambda t: True)
+    monkeypatch.setattr(moe, "_device", lambda: -1)  # where host tensors say they are
+    monkeypatch.setattr(layer.TrainingLayer, "_reads", staticmethod(lambda stream, *tensors: None))
+    n = layer.TrainingLayer.__new__(layer.TrainingLayer)
+    n.calls = []
+    n.pool = Recorder(n.calls, T_max=T, H=H, E=E, P=P, k=K)
+    n.experts = Recorder(n.calls, P=P, H=H, I=I, error_word=torch.zeros(1, dtype=torch.int32))
+    n.experts._gradient = lambda *a: moe.DenseExperts._gradient(n.experts, *a)
+    n.router = n.bias = n.rep_off = n.rep_ids = None
+    n.views, n.kept, n.saved, n.logits = [{"offsets": None, "ex_out": None}], [(None, None)], [None], [None]
+    n.x_rows = n.d_rows = n.h = n.dgu = n.parts = n.row_gates = None
+    n.dgates = torch.zeros(T, K)
+    return n
+
+
+def at(offset, *shape, dtype=torch.float32):
+    """A contiguous tensor that begins `offset` elements behind a 16-byte boundary."""
+    n = 1
+    for s in shape:
+        n *= s
+    return torch.zeros(n + 64, dtype=dtype)[16 + offset:16 + offset + n].view(*shape)
+
+
+def backward_args(**other):
+    return {"dy": at(0, T, H, dtype=BF), "dw13": at(0, P, 2 * I, H), "dw2": at(0, P, H, I), "dx": at(0, T, H, dtype=BF),
+            "dlogits": at(0, T, E), **other}
+
+
+def test_backward_calls(net):
+    net.saved[0] = at(0, T, H, dtype=BF)
+    net.backward(**backward_args())
+    assert net.calls == ["scatter", "down_backward", "down_grad", "up_backward", "scatter", "up_grad", "gather",
+                         "gates_backward"]
+    assert net.saved == [None]
+
+
+BAD = {"dy": at(1, T, H, dtype=BF), "dx": at(4, T, H, dtype=BF), "dlogits": at(1, T, E), "dw13": at(2, P, 2 * I, H),
+       "dw2": at(3, P, H, I)}
+
+
+@pytest.mark.parametrize("name", BAD)
+def test_backward_refuses_odd_addresses_and_enqueues_nothing(net, name):
+    """A row slice of a longer buffer: contiguous, but not on a 16-byte boundary."""
+    net.saved[0] = x = at(0, T, H, dtype=BF)
+    with pytest.raises(ValueError, match=f"{name}: want"):
+        net.backward(**backward_args(**{name: BAD[name]}), accumulate=True)
+    assert net.calls == [] and net.saved[0] is x
+
+
+@pytest.mark.parametrize("name", BAD)
+def test_backward_refuses_tensors_of_another_gpu(net, monkeypatch, name):
+    """(Told by the type and shape in the message: host tensors have one place.)"""
+    net.saved[0] = at(0, T, H, dtype=BF)
+    args = backward_args()
+    real = torch.Tensor.get_device
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is args[name] else real(t))
+    with pytest.raises(ValueError, match="current GPU"):
+        net.backward(**args, accumulate=True)
+    assert net.calls == []
