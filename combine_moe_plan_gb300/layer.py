@@ -72,7 +72,10 @@ class TrainingLayer:
     and ``dw2`` (fp32, added up with ``accumulate``; or bf16).  A replica's weights
     have a gradient of their own.  Several sets may be forward before the first
     goes backward (gradient accumulation, pipelining); the buffers of rows are
-    shared, so all calls go to one stream, or wait for one another."""
+    shared, so all calls go to one stream, or wait for one another.  Tensors are
+    contiguous, on the current GPU and on a 16-byte boundary, of the types and shapes
+    of the calls they go to; others are refused (ValueError) before anything is
+    enqueued."""
 
     def __init__(self, w13, w2, T_max, E, k, router=None, bias=None, rep_off=None, rep_ids=None, n_sets=1):
         if router is None and bias is not None:
@@ -106,8 +109,14 @@ class TrainingLayer:
         moe._dense("logits", logits, torch.float32, (T, p.E))
         if T > p.T_max:
             raise ValueError(f"x: at most {p.T_max} tokens, got {T}")
-        if y is not None:
-            moe._dense("y", y, torch.bfloat16, (T, p.H))
+        if y is None:
+            y = moe._empty((T, p.H), torch.bfloat16, x.device, stream)
+        moe._dense("y", y, torch.bfloat16, (T, p.H))
+        if self.rep_off is not None and self.rep_ids is not None:
+            moe._dense("rep_off", self.rep_off, torch.int32, (p.E + 1,))
+            moe._dense("rep_ids", self.rep_ids, torch.int32, (p.P,))
+        moe._on_one_gpu(ex.error_word, p.workspace, x, logits, y, self.bias, self.rep_off, self.rep_ids)
+        moe._aligned(x=x, logits=logits, y=y)
         self.saved[buf] = None
         self._reads(stream, x, logits)
         if self.router is None:
@@ -118,8 +127,6 @@ class TrainingLayer:
                 self.logits[buf][:T].copy_(logits)
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         v, n = self.views[buf], T * p.k
-        if y is None:
-            y = moe._empty((T, p.H), torch.bfloat16, x.device, stream)
         ex.up(self.x_rows, v["offsets"], self.h, *self.kept[buf], rows=n, stream=stream)
         ex.down(self.h, v["offsets"], v["ex_out"], rows=n, stream=stream)
         y = p.combine(T, y, buf=buf, stream=stream)

@@ -32,7 +32,7 @@ def net(monkeypatch):
     monkeypatch.setattr(layer.TrainingLayer, "_reads", staticmethod(lambda stream, *tensors: None))
     n = layer.TrainingLayer.__new__(layer.TrainingLayer)
     n.calls = []
-    n.pool = Recorder(n.calls, T_max=T, H=H, E=E, P=P, k=K)
+    n.pool = Recorder(n.calls, T_max=T, H=H, E=E, P=P, k=K, workspace=torch.zeros(1))
     n.experts = Recorder(n.calls, P=P, H=H, I=I, error_word=torch.zeros(1, dtype=torch.int32))
     n.experts._gradient = lambda *a: moe.DenseExperts._gradient(n.experts, *a)
     n.router = n.bias = n.rep_off = n.rep_ids = None
@@ -85,4 +85,53 @@ def test_backward_refuses_tensors_of_another_gpu(net, monkeypatch, name):
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is args[name] else real(t))
     with pytest.raises(ValueError, match="current GPU"):
         net.backward(**args, accumulate=True)
+    assert net.calls == []
+
+
+def forward_args(**other):
+    return {"x": at(0, T, H, dtype=BF), "logits": at(0, T, E), "y": at(0, T, H, dtype=BF), **other}
+
+
+def replicas(net, **other):
+    net.rep_off = other.get("rep_off", torch.arange(E + 1, dtype=torch.int32))
+    net.rep_ids = other.get("rep_ids", torch.arange(P, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("with_replicas", [False, True])
+def test_forward_calls(net, with_replicas):
+    if with_replicas:
+        replicas(net)
+    args = forward_args()
+    net.forward(**args)
+    assert net.calls == ["plan", "scatter", "up", "down", "combine"]
+    assert net.saved[0] is args["x"]
+
+
+@pytest.mark.parametrize("name,bad", [("x", at(1, T, H, dtype=BF)), ("logits", at(2, T, E)), ("y", at(4, T, H, dtype=BF))])
+def test_forward_refuses_odd_addresses_and_enqueues_nothing(net, name, bad):
+    with pytest.raises(ValueError, match=f"{name}: want"):
+        net.forward(**forward_args(**{name: bad}))
+    assert net.calls == []
+
+
+@pytest.mark.parametrize("name", ["x", "logits", "y", "rep_off", "rep_ids", "bias"])
+def test_forward_refuses_tensors_of_another_gpu(net, monkeypatch, name):
+    replicas(net)
+    net.bias = torch.zeros(E)
+    args = forward_args()
+    there = args.get(name, getattr(net, name, None))
+    real = torch.Tensor.get_device
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is there else real(t))
+    with pytest.raises(ValueError, match="current GPU"):
+        net.forward(**args)
+    assert net.calls == []
+
+
+@pytest.mark.parametrize("bad", [dict(rep_off=torch.arange(E + 1)), dict(rep_off=torch.zeros(E, dtype=torch.int32)),
+                                 dict(rep_ids=torch.arange(P)), dict(rep_ids=torch.zeros(P - 1, dtype=torch.int32)),
+                                 dict(rep_ids=torch.zeros(2 * P, dtype=torch.int32)[::2])], ids=str)
+def test_forward_refuses_a_replica_map_that_the_plan_would_misread(net, bad):
+    replicas(net, **bad)
+    with pytest.raises(ValueError, match=f"{next(iter(bad))}: want"):
+        net.forward(**forward_args())
     assert net.calls == []
