@@ -117,6 +117,8 @@ class TrainingLayer:
             moe._dense("rep_ids", self.rep_ids, torch.int32, (p.P,))
         moe._on_one_gpu(ex.error_word, p.workspace, x, logits, y, self.bias, self.rep_off, self.rep_ids)
         moe._aligned(x=x, logits=logits, y=y)
+        if _overlap(x, y):
+            raise ValueError("y lies in x, which is kept for the backward pass")
         self.saved[buf] = None
         self._reads(stream, x, logits)
         if self.router is None:
@@ -176,6 +178,12 @@ class TrainingLayer:
     def check(self) -> int:
         """Wait, and return the device error bits of the pool and the experts (0 = clean)."""
         return self.pool.check() | self.experts.check()
+
+
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    begin, end = (max(t.data_ptr() for t in (a, b)), min(t.data_ptr() + t.numel() * t.element_size() for t in (a, b)))
+    return begin < end
 
 
 def random_experts(P, H, I, seed=0, device="cuda"):

@@ -135,3 +135,13 @@ def test_forward_refuses_a_replica_map_that_the_plan_would_misread(net, bad):
     with pytest.raises(ValueError, match=f"{next(iter(bad))}: want"):
         net.forward(**forward_args())
     assert net.calls == []
+
+
+def test_forward_refuses_to_write_over_what_it_keeps(net):
+    both = at(0, 2 * T, H, dtype=BF)
+    for x, y in ((both[:T], both[:T]), (both[:T], both[T // 2:T // 2 + T]), (both[T // 2:T // 2 + T], both[:T])):
+        with pytest.raises(ValueError, match="kept"):
+            net.forward(**forward_args(x=x, y=y))
+    assert net.calls == []
+    net.forward(**forward_args(x=both[:T], y=both[T:]))
+    assert net.calls
