@@ -8,7 +8,10 @@
 // gates_backward_kernel: one warp per token.  A copy's partial sums are added by a
 // power-of-two run of lanes, several copies side by side, always in the same
 // order; lane j then holds dg_j, and the router's gradient needs two sums over the
-// token's copies (and, for softmax scores, over its logits).
+// token's copies (and, for softmax scores, over its logits).  Renormalised scores are
+// divided by their sum S before anything else: r_j = s_j / S is at most 1, where
+// (dg_j - sum_i dg_i r_i) / S overflows once all scores of a token are tiny, although
+// its product with s_j is of dg's size.
 #include "moe_internal.h"
 #include "ptx.cuh"
 
@@ -139,23 +142,24 @@ gates_backward_kernel(const float* __restrict__ logits, const float* __restrict_
     const float s = !chosen                    ? 0.0f
                     : KIND == Gates::kSigmoid  ? finite_or_zero(1.0f / (1.0f + expf(-mine)))
                                                : finite_or_zero(expf(mine - top) / total);
-    float ds = scale * dg;
+    // ds_j s_j of a chosen copy
+    float dss = scale * dg * s;
     if (renorm) {
         const float sum = warp_sum(s);
-        const float mean = warp_sum(ds * s) / sum;
-        ds = chosen && sum > 0.0f ? (ds - mean) / sum : 0.0f;
+        const float r = sum > 0.0f ? s / sum : 0.0f;
+        dss = scale * (dg - warp_sum(dg * r)) * r;
     }
-    if constexpr (KIND == Gates::kSigmoid) {
+    if (KIND == Gates::kSigmoid || renorm) {  // (the sum of dss is 0 with renorm, so that the others have no part in a softmax)
         for (int e = lane; e < E; e += 32) out[e] = 0.0f;
         __syncwarp();
-        if (chosen) out[my_e] = ds * s * (1.0f - s);
+        if (chosen) out[my_e] = KIND == Gates::kSigmoid ? dss * (1.0f - s) : dss;
     } else {
-        const float mean = warp_sum(ds * s);
+        const float mean = warp_sum(dss);
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
             if (lane + 32 * i < E) out[lane + 32 * i] = -finite_or_zero(l[i] / total) * mean;
         __syncwarp();
-        if (chosen) out[my_e] = s * (ds - mean);
+        if (chosen) out[my_e] = dss - s * mean;
     }
 }
 

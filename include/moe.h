@@ -444,7 +444,9 @@ MOE_API int moe_gather(moe_pool* pool, const uint16_t* rows, uint16_t* y, int32_
  * set's gates.  moe_plan_routed, S the sum of the token's chosen scores s_j: with
  * renorm ds_j = scale / S (dg_j - sum_i dg_i s_i / S) (0 where S is 0), without
  * ds_j = scale dg_j; sigmoid: dl_j = ds_j s_j (1 - s_j) for the chosen; softmax:
- * dl_e = s_e (ds_e - sum_j ds_j s_j) for all experts, ds_e = 0 where not chosen.
+ * dl_e = s_e (ds_e - sum_j ds_j s_j) for all experts, ds_e = 0 where not chosen
+ * (with renorm the sum is 0, and so is dl_e of those).  1 / S is not formed: scores
+ * of any size give gradients of the size of dg.
  * Which experts were chosen, and with them the balance bias and the groups, has no
  * gradient.  MOE_ERR_STATE if the set was not planned with this T, or by the other
  * kind of plan; T and the kind are those of the last plan called on the set,
