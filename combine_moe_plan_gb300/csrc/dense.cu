@@ -94,20 +94,21 @@ enum class Op { kUp, kDown, kDownBack, kUpBack, kGrad };
 // Steps that are summed in TMEM before the sums go to registers.  The tensor cores
 // cut their sums off instead of rounding them, which shortens a sum by about
 // 2.4e-8 of it for every 16 terms (four times that where all terms have one sign).
-// Every product is therefore summed 512 terms at a time (768 in down_back, whose
-// finishing takes longer than the products of two times 512 do), and those sums are
-// added up in registers, rounded to nearest.  Results in bf16 need it as much as those
+// Every product is therefore summed 512 terms at a time (448 in grad, 768 in
+// down_back, whose finishing takes longer than the products of two times 512 do), and
+// those sums are added up in registers, rounded to nearest.  Results in bf16 need it as much as those
 // in fp32: an inner size of 131,072 summed in one go came out short by 7.8e-4 on
 // average, a fifth of a bf16 step.  It costs them nothing (98,304 rows over 64 experts
 // of 2048 x 1024, up_back 469 us and 468 in one go, down 250 / 249).  The same rows,
-// relative error of up_grad and of down_back's parts (fp32 sums: 3.7e-7 and 4e-7), and
-// us of up, down_back and up_grad at the power limit:
-//    256 terms  2.3e-7  2.8e-7  595  441  642
-//    512        4.5e-7  4.9e-7  553  392 to 406  611
-//    768                6.9e-7       377
-//   1024        9.0e-7  1.0e-6  551  376 to 388  606
-//   all         2.6e-6  2.1e-6  549  386  605
-__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDownBack ? 12 : 8; }
+// relative error of up_grad and of down_back's parts (torch's fp32 products: 4.2e-7 and
+// 4.0e-7), and us of up_grad and down_back from a cool GPU:
+//    256 terms  2.3e-7  2.8e-7  555  429
+//    320        2.8e-7  3.2e-7  540  417
+//    384        3.4e-7  3.7e-7  531  403
+//    448        4.0e-7          523
+//    512        4.5e-7  4.9e-7  523  379
+//    768                6.9e-7       363
+__host__ __device__ constexpr int chunk_of(Op op) { return op == Op::kDownBack ? 12 : op == Op::kGrad ? 7 : 8; }
 
 struct alignas(16) Barriers {
     uint64_t full[kMostStages], empty[kMostStages];  // stages; full: both CTAs', in the first
