@@ -19,6 +19,7 @@ forward and backward:
 from __future__ import annotations
 
 import argparse
+import contextlib
 
 import torch
 
@@ -86,7 +87,8 @@ class TrainingLayer:
         self.views = [self.pool.view(b) for b in range(n_sets)]
         n, dev = T_max * k, ex.error_word.device
         self.kept = [ex.kept(n) for _ in range(n_sets)]
-        self.saved = [None] * n_sets
+        self.saved = [None] * n_sets  # x, the logits kept, and the handle of the stream that reads x
+        self._streams = {}
         # the logits as the plan saw them: the caller's may be those of the next batch by the time of a backward
         self.logits = [torch.empty((T_max, E), device=dev) if router is not None else None for _ in range(n_sets)]
 
@@ -117,29 +119,30 @@ class TrainingLayer:
             moe._dense("rep_ids", self.rep_ids, torch.int32, (p.P,))
         moe._on_one_gpu(ex.error_word, p.workspace, x, logits, y, self.bias, self.rep_off, self.rep_ids)
         moe._aligned(x=x, logits=logits, y=y)
-        if _overlap(x, y):
+        if abs(x.data_ptr() - y.data_ptr()) < 2 * T * p.H:
             raise ValueError("y lies in x, which is kept for the backward pass")
         self.saved[buf] = None
-        self._reads(stream, x, logits)
+        on = self._reads(stream, x, logits)
         if self.router is None:
             p.plan(logits, self.rep_off, self.rep_ids, buf=buf, stream=stream)
         else:
             p.plan_routed(logits, self.router, self.bias, self.rep_off, self.rep_ids, buf=buf, stream=stream)
-            with torch.cuda.stream(stream):  # (None: the current one)
-                self.logits[buf][:T].copy_(logits)
+            kept = self.logits[buf] if T == p.T_max else self.logits[buf][:T]
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                logits = kept.copy_(logits)
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         v, n = self.views[buf], T * p.k
         ex.up(self.x_rows, v["offsets"], self.h, *self.kept[buf], rows=n, stream=stream)
         ex.down(self.h, v["offsets"], v["ex_out"], rows=n, stream=stream)
         y = p.combine(T, y, buf=buf, stream=stream)
-        self.saved[buf] = x
+        self.saved[buf] = x, logits if self.router is not None else None, on
         return y
 
     def backward(self, dy, dw13, dw2, dx=None, dlogits=None, accumulate=False, buf=0, stream=None):
         p, ex = self.pool, self.experts
         if not 0 <= buf < len(self.saved) or self.saved[buf] is None:
             raise ValueError(f"set {buf} has no forward to go back through")
-        x = self.saved[buf]
+        x, logits, on = self.saved[buf]
         T, n = x.shape[0], x.shape[0] * p.k
         dx = moe._empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
         dlogits = moe._empty((T, p.E), torch.float32, x.device, stream) if dlogits is None else dlogits
@@ -151,7 +154,8 @@ class TrainingLayer:
         ex._gradient("dw2", dw2, ex.H, ex.I, accumulate)
         moe._on_one_gpu(ex.error_word, dy, dx, dlogits, dw13, dw2)
         moe._aligned(dy=dy, dx=dx, dlogits=dlogits, dw13=dw13, dw2=dw2)
-        self._reads(stream, dy, x)
+        if self._reads(stream, dy) != on:
+            self._reads(stream, x)
         offsets, (codes, scales) = self.views[buf]["offsets"], self.kept[buf]
         p.scatter(dy, self.d_rows, self.row_gates, buf=buf, stream=stream)
         hg = self.h  # the forward's h has been read
@@ -162,28 +166,26 @@ class TrainingLayer:
         p.scatter(x, self.x_rows, buf=buf, stream=stream)
         ex.up_grad(self.dgu, self.x_rows, offsets, dw13, accumulate, rows=n, stream=stream)
         p.gather(T, self.d_rows, dx, buf=buf, stream=stream)
-        routed = (None, None) if self.router is None else (self.router, self.logits[buf][:T])
-        p.gates_backward(T, self.parts, self.dgates[:T], dlogits, *routed, buf=buf, stream=stream)
+        dgates = self.dgates if T == p.T_max else self.dgates[:T]
+        p.gates_backward(T, self.parts, dgates, dlogits, self.router, logits, buf=buf, stream=stream)
         self.saved[buf] = None
         return dx, dlogits
 
-    @staticmethod
-    def _reads(stream, *tensors):
+    def _reads(self, stream, *tensors):
         """``stream`` (None: the current one) reads these: their memory is not handed out again before it has,
-        even if the layer's is the last reference and is let go of while that work is still queued."""
-        s = torch.cuda.current_stream() if stream is None else stream
+        even if the layer's is the last reference and is let go of while that work is still queued.  Returns the
+        stream's handle."""
+        on = moe._stream(stream)
+        s = stream
+        if s is None and (s := self._streams.get(on)) is None:  # a torch Stream takes as long to make as a call
+            s = self._streams[on] = torch.cuda.current_stream()
         for t in tensors:
             t.record_stream(s)
+        return on
 
     def check(self) -> int:
         """Wait, and return the device error bits of the pool and the experts (0 = clean)."""
         return self.pool.check() | self.experts.check()
-
-
-def _overlap(a, b):
-    """Whether two contiguous tensors share memory."""
-    begin, end = (max(t.data_ptr() for t in (a, b)), min(t.data_ptr() + t.numel() * t.element_size() for t in (a, b)))
-    return begin < end
 
 
 def random_experts(P, H, I, seed=0, device="cuda"):

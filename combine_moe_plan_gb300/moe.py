@@ -619,7 +619,7 @@ def _on_one_gpu(*tensors):
 def _aligned(**tensors):
     """Every tensor begins on a 16-byte boundary, as the kernels want it."""
     for name, t in tensors.items():
-        if t.data_ptr() % 16:
+        if t.data_ptr() & 15:
             raise ValueError(f"{name}: want a tensor on a 16-byte boundary, got one at {t.data_ptr():#x}")
 
 

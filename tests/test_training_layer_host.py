@@ -29,7 +29,7 @@ def net(monkeypatch):
     """A TrainingLayer after a forward of T tokens, whose calls are noted."""
     monkeypatch.setattr(moe, "_on_gpu", lambda t: True)
     monkeypatch.setattr(moe, "_device", lambda: -1)  # where host tensors say they are
-    monkeypatch.setattr(layer.TrainingLayer, "_reads", staticmethod(lambda stream, *tensors: None))
+    monkeypatch.setattr(layer.TrainingLayer, "_reads", lambda self, stream, *tensors: 0)
     n = layer.TrainingLayer.__new__(layer.TrainingLayer)
     n.calls = []
     n.pool = Recorder(n.calls, T_max=T, H=H, E=E, P=P, k=K, workspace=torch.zeros(1))
@@ -50,13 +50,18 @@ def at(offset, *shape, dtype=torch.float32):
     return torch.zeros(n + 64, dtype=dtype)[16 + offset:16 + offset + n].view(*shape)
 
 
+def kept():
+    """What a forward leaves for the backward: x, no logits (there is no router), a stream."""
+    return at(0, T, H, dtype=BF), None, 0
+
+
 def backward_args(**other):
     return {"dy": at(0, T, H, dtype=BF), "dw13": at(0, P, 2 * I, H), "dw2": at(0, P, H, I), "dx": at(0, T, H, dtype=BF),
             "dlogits": at(0, T, E), **other}
 
 
 def test_backward_calls(net):
-    net.saved[0] = at(0, T, H, dtype=BF)
+    net.saved[0] = kept()
     net.backward(**backward_args())
     assert net.calls == ["scatter", "down_backward", "down_grad", "up_backward", "scatter", "up_grad", "gather",
                          "gates_backward"]
@@ -70,16 +75,16 @@ BAD = {"dy": at(1, T, H, dtype=BF), "dx": at(4, T, H, dtype=BF), "dlogits": at(1
 @pytest.mark.parametrize("name", BAD)
 def test_backward_refuses_odd_addresses_and_enqueues_nothing(net, name):
     """A row slice of a longer buffer: contiguous, but not on a 16-byte boundary."""
-    net.saved[0] = x = at(0, T, H, dtype=BF)
+    net.saved[0] = saved = kept()
     with pytest.raises(ValueError, match=f"{name}: want"):
         net.backward(**backward_args(**{name: BAD[name]}), accumulate=True)
-    assert net.calls == [] and net.saved[0] is x
+    assert net.calls == [] and net.saved[0] is saved
 
 
 @pytest.mark.parametrize("name", BAD)
 def test_backward_refuses_tensors_of_another_gpu(net, monkeypatch, name):
     """(Told by the type and shape in the message: host tensors have one place.)"""
-    net.saved[0] = at(0, T, H, dtype=BF)
+    net.saved[0] = kept()
     args = backward_args()
     real = torch.Tensor.get_device
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is args[name] else real(t))
@@ -104,7 +109,7 @@ def test_forward_calls(net, with_replicas):
     args = forward_args()
     net.forward(**args)
     assert net.calls == ["plan", "scatter", "up", "down", "combine"]
-    assert net.saved[0] is args["x"]
+    assert net.saved[0][0] is args["x"]
 
 
 @pytest.mark.parametrize("name,bad", [("x", at(1, T, H, dtype=BF)), ("logits", at(2, T, E)), ("y", at(4, T, H, dtype=BF))])
