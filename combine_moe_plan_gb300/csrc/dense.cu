@@ -29,25 +29,26 @@
 // is written by TMA and counted at the issuing CTA's barrier, so that nothing is handed
 // from a thread of one CTA to one of the other.  (A warp that cleared the rows behind a
 // window in shared memory would have to publish them to the other CTA, release.cluster,
-// 1000 to 2200 cycles a tile: 49.5 us of 1537 tokens over 44 experts in bf16; boxes of
-// exactly the rows left, and of zeros behind them, sixteen loads a tile, 50.2.)
+// 1000 to 2200 cycles a tile: 1537 tokens over 44 experts in bf16 49.5 us that way, 40.7
+// this way, and 50.2 with boxes of exactly the rows left and of zeros behind them, sixteen
+// loads a tile.)
 //
 // What bounds it (one GB300; 98,304 rows over 64 experts of 2048 x 1024 unless named).
 //   up, up_back: the tensor pipe, 92 and 91 % of it active, 544 and 543 cycles a stage
 // of 512; from a cool GPU 480 and 472 us (1.72 and 1.75 PFLOP/s, the rows that fill the
 // last tile of a window not counted), at the power limit, 1.4 to 1.5 GHz, 552 and 533.
 // cuBLAS, 8192 cubed, on the same box: 1.88 and 1.72 PFLOP/s.
-//   grad in fp32: 520 to 530 us cool, 575 to 600 hot.  Its stores (1.07 GB) cost 85 us of
+//   grad in fp32: 523 to 553 us cool, 575 to 629 hot (GPUs of two kinds of cooling).  Its stores (1.07 GB) cost 85 us of
 // it, operands that miss L2 40: stores and loads get in each other's way between SM and
 // L2 (43 bytes a cycle in, 7 out).  Stores through the load-store unit instead of TMA
 // save nothing, 32 bytes a lane straight from registers cost 70 us more.
-//   down_back: 366 us cool, 377 hot; half of the tensor pipe.  Finishing tiles costs 100
+//   down_back: 363 to 371 us cool, 377 to 402 hot; half of the tensor pipe.  Finishing tiles costs 100
 // us: codes in, three outputs out, 16 us of arithmetic.
 //   Few rows an expert: HBM.  One token over 256 experts of 7168 x 2048, first product
 // 77 us (69 at the copy peak), 96 tokens, second product 897 us (6.4 GB: 1.06 of the copy
 // peak); 4096 tokens over 288, first product 2,623 (1.00).
-//   More stages shorten everything (grad of 24,576 rows in bf16: 185 us with 6, 203 with
-// 5, 250 with 3), so outputs have one box a warp.
+//   More stages shorten everything (grad of 24,576 rows in bf16: 162 us with 6, 170 with
+// 5, 218 with 3), so outputs have one box a warp.
 //   Measured and left out: L2 prefetches of the operands 8 to 16 stages ahead (603 / 603
 // us of grad, 420 / 410 of down_back); 16 finishing warps in down_back (493 / 413);
 // its boxes 64 bytes wide with a stage more (448 / 413), or two of them (418 / 381); tiles
@@ -827,7 +828,11 @@ int launch_form(Problem pr, const uint16_t* a, const uint16_t* w, cudaStream_t s
 // time, and single CTAs are faster.  Single CTAs / pairs: up of 1 token over 256
 // experts of 7168 x 2048 80.1 / 86.8 us, down of 96 tokens 933 / 1000, up of 1024
 // tokens over 64 such experts (128 rows each) 606 / 652; 1537 tokens over 44 experts
-// of 1920 x 896 (175 rows each) up 68.5 / 67.5, up_back 71.3 / 67.4.
+// of 1920 x 896 (175 rows each) up 68.5 / 67.5, up_back 71.3 / 67.4.  The rule knows
+// the average alone (the windows are on the device).  Where the same rows fill a few
+// long windows, pairs would be faster: 8192 rows over 64 experts of 7168 x 2048 (the
+// rule's border) in all 64 windows, up 567 / 602; in 16 of them 310 / 274, in 2
+// 300 / 261; of 2048 x 1024, 96 / 98, 57 / 50, 47 / 43.
 template <Op OP>
 int launch_dense(const Problem& pr, const uint16_t* a, const uint16_t* w, cudaStream_t s) {
     if constexpr (OP == Op::kUp || OP == Op::kDown || OP == Op::kUpBack)

@@ -417,6 +417,9 @@ MOE_API int moe_combine(moe_pool* pool, const uint16_t* ex_out, uint16_t* y, int
  * terms of both signs that leaves a relative error, root mean square over a tensor, of
  * 4.5e-7 in a weights' gradient and of 8e-7 in gate_parts (a product in plain fp32: 2.4e-7
  * to 4.2e-7); at most it is 6e-6 of the sum of the terms' sizes.
+ *   moe_dense_down_backward, the weights' gradients and, where a window has more than 128
+ * rows on average, moe_dense_up, _down and _up_backward run on clusters of two CTAs:
+ * MOE_ERR_CUDA on a device or partition that refuses those.
  */
 
 /*
